@@ -18,6 +18,11 @@ Entry points (same names as the C ABI):
     la_swa_forward(q, k, v, window, *, out=None, lse=False) -> dict
     la_swa_cache_fill(k, v, window) -> (k_cache, v_cache)
     la_swa_decode_step(q, k, v, k_cache, v_cache, pos, window, y=None) -> y
+    la_paged_cache_fill(k, v, k_pages, v_pages, block_table, lens, *, n_new=None, weights=None,
+                        positions=None, pos=None) -> (k_pages, v_pages)
+    la_paged_decode_step(q, k, v, k_pages, v_pages, block_table, lens, *, y=None, lse=None, weights=None,
+                         weights_out=None, positions=None, pos=None) -> y
+    la_paged_evict(k_pages, v_pages, block_table, lens, weights, budget, *, recent=0, ...) -> lens
     la_feature_map(x, fmap) -> phi
     la_feature_dim(fmap, dqk) -> int
     la_get_device_status() -> None (raises on a recorded device error)
@@ -105,6 +110,18 @@ def load_library(path: str | None = None):
     lib.la_swa_decode_step.restype = i
     lib.la_swa_kernel_plan.argtypes = [i] * 8 + [ctypes.c_char_p, sz]
     lib.la_swa_kernel_plan.restype = i
+    lib.la_paged_cache_fill.argtypes = [vp] * 10 + [i] * 9 + [vp]
+    lib.la_paged_cache_fill.restype = i
+    lib.la_paged_decode_workspace_bytes.argtypes = [i] * 9
+    lib.la_paged_decode_workspace_bytes.restype = sz
+    lib.la_paged_decode_step.argtypes = [vp] * 14 + [sz] + [i] * 9 + [vp]
+    lib.la_paged_decode_step.restype = i
+    lib.la_paged_evict_workspace_bytes.argtypes = [i] * 5
+    lib.la_paged_evict_workspace_bytes.restype = sz
+    lib.la_paged_evict.argtypes = [vp] * 11 + [sz] + [i] * 10 + [vp]
+    lib.la_paged_evict.restype = i
+    lib.la_paged_kernel_plan.argtypes = [i] * 10 + [ctypes.c_char_p, sz]
+    lib.la_paged_kernel_plan.restype = i
     lib.la_kernel_plan.argtypes = [i] * 8 + [ctypes.c_char_p, sz]
     lib.la_kernel_plan.restype = i
     lib.la_selftest_bounded_wait.argtypes = [ctypes.c_uint, vp]
@@ -442,6 +459,142 @@ def la_swa_decode_step(q, k, v, k_cache, v_cache, pos, window, y=None):
           _ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(k_cache), _ptr(v_cache), _ptr(pos), B, H, dqk, dv, int(window),
           _dtype_code(q))
     return y
+
+
+def _paged_cache(k_pages, v_pages, block_table, lens):
+    """Sizes of a paged cache after checking that its four tensors agree:
+    (num_pages, Hkv, page_size, dqk, dv, B, max_pages, dtype code)."""
+    P, Hkv, page, dqk = k_pages.shape
+    dv = v_pages.shape[-1]
+    B, max_pages = block_table.shape
+    _expect("v_pages", v_pages, (P, Hkv, page, dv), k_pages.dtype, k_pages.device)
+    _expect("block_table", block_table, (B, max_pages), torch.int32, k_pages.device)
+    _expect("lens", lens, (B,), torch.int32, k_pages.device)
+    return P, Hkv, page, dqk, dv, B, max_pages, _dtype_code(k_pages)
+
+
+def la_paged_cache_fill(k, v, k_pages, v_pages, block_table, lens, *, n_new=None, weights=None, positions=None,
+                        pos=None):
+    """Append k, v [B,Hkv,N,*] to a paged cache: slot lens[b] + i takes token i,
+    for i < n_new[b] (all N without n_new).  k_pages [P,Hkv,page,dqk] and v_pages
+    [P,Hkv,page,dv] are written in place; block_table int32 [B,max_pages]; lens
+    int32 [B] (not advanced here).  weights fp32 and positions int32
+    [B,Hkv,max_pages*page]: 0 and pos[b] + i are written for the new slots.
+    Returns (k_pages, v_pages)."""
+    lib = load_library()
+    P, Hkv, page, dqk, dv, B, max_pages, dt = _paged_cache(k_pages, v_pages, block_table, lens)
+    dev, N = k_pages.device, k.shape[2]
+    slots = (B, Hkv, max_pages * page)
+    _expect("k", k, (B, Hkv, N, dqk), k_pages.dtype, dev)
+    _expect("v", v, (B, Hkv, N, dv), k_pages.dtype, dev)
+    _expect("n_new", n_new, (B,), torch.int32, dev)
+    _expect("weights", weights, slots, torch.float32, dev)
+    _expect("positions", positions, slots, torch.int32, dev)
+    _expect("pos", pos, (B,), torch.int32, dev)
+    if (positions is None) != (pos is None):
+        raise ValueError("positions and pos go together")
+    _dev(k, v, k_pages, v_pages, block_table, lens, n_new, weights, positions, pos)
+    _call(lib.la_paged_cache_fill, "la_paged_cache_fill", dev,
+          _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(lens), _ptr(n_new), _ptr(weights),
+          _ptr(positions), _ptr(pos), B, Hkv, N, dqk, dv, P, page, max_pages, dt)
+    return k_pages, v_pages
+
+
+def la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page_size, max_pages, with_weights, dtype) -> int:
+    return int(load_library().la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page_size, max_pages,
+                                                              int(with_weights), dtype))
+
+
+def la_paged_decode_step(q, k, v, k_pages, v_pages, block_table, lens, *, y=None, lse=None, weights=None,
+                         weights_out=None, positions=None, pos=None, workspace=None):
+    """Softmax attention of one new token over a paged cache.  q [B,Hq,dqk],
+    Hq a multiple of Hkv; k [B,Hkv,dqk] and v [B,Hkv,dv] are stored in slot
+    lens[b] first and attended to (lens is not advanced here), or both None to
+    attend to the cache as it is.  lse fp32 [B,Hq], if given, is written.  With
+    weights fp32 [B,Hkv,max_pages*page] the attention weight that each slot
+    receives is added, into weights_out if given, else in place.  positions
+    int32 (same shape) with pos int32 [B]: pos[b] is written for the new slot.
+    Returns y [B,Hq,dv]."""
+    lib = load_library()
+    P, Hkv, page, dqk, dv, B, max_pages, dt = _paged_cache(k_pages, v_pages, block_table, lens)
+    dev, Hq = q.device, q.shape[1]
+    slots = (B, Hkv, max_pages * page)
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    if (positions is None) != (pos is None):
+        raise ValueError("positions and pos go together")
+    if positions is not None and k is None:
+        raise ValueError("positions need a new token (k, v)")
+    if weights_out is not None and weights is None:
+        raise ValueError("weights_out needs weights")
+    _expect("q", q, (B, Hq, dqk), k_pages.dtype, k_pages.device)
+    _expect("k", k, (B, Hkv, dqk), q.dtype, dev)
+    _expect("v", v, (B, Hkv, dv), q.dtype, dev)
+    _expect("y", y, (B, Hq, dv), q.dtype, dev)
+    _expect("lse", lse, (B, Hq), torch.float32, dev)
+    _expect("weights", weights, slots, torch.float32, dev)
+    _expect("weights_out", weights_out, slots, torch.float32, dev)
+    _expect("positions", positions, slots, torch.int32, dev)
+    _expect("pos", pos, (B,), torch.int32, dev)
+    wsb = la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page, max_pages, weights is not None, dt)
+    workspace, wsb = _workspace(workspace, wsb, dev)
+    _dev(q, k, v, k_pages, v_pages, block_table, lens, y, lse, weights, weights_out, positions, pos)
+    if weights_out is None:
+        weights_out = weights
+    if y is None:
+        y = torch.empty(B, Hq, dv, dtype=q.dtype, device=dev)
+    _call(lib.la_paged_decode_step, "la_paged_decode_step", dev,
+          _ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(lse), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(lens),
+          _ptr(weights), _ptr(weights_out), _ptr(positions), _ptr(pos), _ptr(workspace), wsb, B, Hq, Hkv, dqk, dv, P,
+          page, max_pages, dt)
+    return y
+
+
+def la_paged_evict_workspace_bytes(B, Hkv, page_size, max_pages, budget) -> int:
+    return int(load_library().la_paged_evict_workspace_bytes(B, Hkv, page_size, max_pages, budget))
+
+
+def la_paged_evict(k_pages, v_pages, block_table, lens, weights, budget, *, recent=0, positions=None, pos=None,
+                   lens_out=None, weights_out=None, positions_out=None, workspace=None):
+    """Keep `budget` slots of every (b, h) that holds more: the tokens of the
+    last `recent` positions, then those of largest accumulated weight; kept
+    slots at or above `budget` move into dropped ones below it (k_pages,
+    v_pages in place).  weights fp32 and positions int32 [B,Hkv,max_pages*page]
+    and lens int32 [B] are updated in place unless the *_out tensors are given.
+    positions and pos int32 [B] are required when recent > 0.  Returns the new
+    lens."""
+    lib = load_library()
+    P, Hkv, page, dqk, dv, B, max_pages, dt = _paged_cache(k_pages, v_pages, block_table, lens)
+    dev, budget, recent = k_pages.device, int(budget), int(recent)
+    slots = (B, Hkv, max_pages * page)
+    if recent > 0 and (positions is None or pos is None):
+        raise ValueError("recent > 0 needs positions and pos")
+    if positions_out is not None and positions is None:
+        raise ValueError("positions_out needs positions")
+    _expect("weights", weights, slots, torch.float32, dev)
+    _expect("weights_out", weights_out, slots, torch.float32, dev)
+    _expect("positions", positions, slots, torch.int32, dev)
+    _expect("positions_out", positions_out, slots, torch.int32, dev)
+    _expect("pos", pos, (B,), torch.int32, dev)
+    _expect("lens_out", lens_out, (B,), torch.int32, dev)
+    workspace, wsb = _workspace(workspace, la_paged_evict_workspace_bytes(B, Hkv, page, max_pages, budget), dev)
+    _dev(k_pages, v_pages, block_table, lens, weights, weights_out, positions, positions_out, pos, lens_out)
+    lens_out = lens if lens_out is None else lens_out
+    weights_out = weights if weights_out is None else weights_out
+    positions_out = positions if positions_out is None else positions_out
+    _call(lib.la_paged_evict, "la_paged_evict", dev,
+          _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(lens), _ptr(lens_out), _ptr(weights),
+          _ptr(weights_out), _ptr(positions), _ptr(positions_out), _ptr(pos), _ptr(workspace), wsb, B, Hkv, dqk, dv,
+          P, page, max_pages, budget, recent, dt)
+    return lens_out
+
+
+def la_paged_kernel_plan(op: int, B, Hq, Hkv, dqk, dv, page_size, max_pages, with_weights, dtype):
+    """(number of kernel launches, [kernel names]) of a paged call: op 0 fill, 1 decode step, 2 evict."""
+    buf = ctypes.create_string_buffer(256)
+    n = load_library().la_paged_kernel_plan(op, B, Hq, Hkv, dqk, dv, page_size, max_pages, int(with_weights), dtype,
+                                            buf, len(buf))
+    return n, [x for x in buf.value.decode().split(",") if x]
 
 
 def la_feature_map(x, fmap):

@@ -24,6 +24,7 @@
 #include "la_bwd_sm100.cuh"
 #include "la_fwd_split_sm100.cuh"
 #include "la_swa.cuh"
+#include "la_paged.cuh"
 
 using namespace la;
 
@@ -748,6 +749,60 @@ static bool overlaps(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
+// Sizes of the paged calls.  Rows are 32-bit indices, elements 64-bit offsets.
+static la_status check_paged(int B, int Hq, int Hkv, int dqk, int dv, int num_pages, int page_size, int max_pages,
+                             int dtype)
+{
+    if (B < 1 || Hq < 1 || Hkv < 1 || dqk < 1 || dv < 1 || num_pages < 1 || page_size < 1 || max_pages < 1)
+        return LA_ERR_INVALID_ARG;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (Hq % Hkv) return LA_ERR_INVALID_ARG;
+    const int64_t lim = (int64_t)1 << 31;
+    if ((int64_t)num_pages * Hkv >= lim || (int64_t)num_pages * Hkv * page_size >= lim) return LA_ERR_INVALID_ARG;
+    if ((int64_t)max_pages * page_size >= lim) return LA_ERR_INVALID_ARG;
+    if ((int64_t)B * Hq * (dqk > dv ? dqk : dv) >= lim) return LA_ERR_INVALID_ARG;
+    if (dqk > 128 || dv > 128) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+static PagedCache make_paged(void *kp, void *vp, const int32_t *table, const int32_t *lens, int B, int Hkv, int dqk,
+                             int dv, int num_pages, int page_size, int max_pages)
+{
+    PagedCache c;
+    c.kp = kp;
+    c.vp = vp;
+    c.table = table;
+    c.lens = lens;
+    c.B = B;
+    c.Hkv = Hkv;
+    c.dqk = dqk;
+    c.dv = dv;
+    c.num_pages = num_pages;
+    c.page = page_size;
+    c.max_pages = max_pages;
+    c.shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (page_size == 1 << i) c.shift = i;
+    return c;
+}
+
+static size_t elem_size(int dtype) { return dtype == LA_F32 ? 4 : 2; }
+static bool rows16(int d, int dtype) { return d * elem_size(dtype) % 16 == 0; }
+
+// The cache's own arguments, shared by the three calls.
+static la_status check_paged_ptrs(const void *kp, const void *vp, const int32_t *table, const int32_t *lens)
+{
+    if (!kp || !vp || !table || !lens) return LA_ERR_INVALID_ARG;
+    if (!aligned(kp, 16) || !aligned(vp, 16) || !aligned(table, 4) || !aligned(lens, 4)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+// An input and output of the same size: one buffer, or two that do not overlap.
+static bool same_or_apart(const void *in, const void *out, size_t bytes)
+{
+    return in == out || !overlaps(in, bytes, out, bytes);
+}
+
 la_status la_forward_from_state(const void *q, const void *k, const void *v, void *o, const float *s_in,
                                 const float *z_in, float *s_out, float *z_out, float *den_out, void *workspace,
                                 size_t workspace_bytes, int B, int H, int N, int dqk, int dv, int fmap,
@@ -1094,6 +1149,166 @@ la_status la_swa_decode_step(const void *q, const void *k, const void *v, void *
             (__nv_bfloat16 *)k_cache, (__nv_bfloat16 *)v_cache, pos, H, dqk, dv, window, scale);
     }
     return launch_status();
+}
+
+la_status la_paged_cache_fill(const void *k, const void *v, void *k_pages, void *v_pages, const int32_t *block_table,
+                              const int32_t *lens, const int32_t *n_new, float *weights, int32_t *positions,
+                              const int32_t *pos, int B, int Hkv, int N, int dqk, int dv, int num_pages,
+                              int page_size, int max_pages, int dtype, void *stream)
+{
+    if (N < 1) return LA_ERR_INVALID_ARG;
+    const la_status sh = check_paged(B, Hkv, Hkv, dqk, dv, num_pages, page_size, max_pages, dtype);
+    if (sh != LA_OK) return sh;
+    const la_status pt = check_paged_ptrs(k_pages, v_pages, block_table, lens);
+    if (pt != LA_OK) return pt;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(n_new, 4) || !aligned(weights, 4) ||
+        !aligned(positions, 4) || !aligned(pos, 4) || (positions == nullptr) != (pos == nullptr))
+        return LA_ERR_INVALID_ARG;
+    const int64_t blocks = (int64_t)B * Hkv * (((int64_t)N + kPagedFillRows - 1) / kPagedFillRows);
+    if (blocks >= (int64_t)1 << 31) return LA_ERR_INVALID_ARG;
+    if (check_on_current_device(k_pages) != LA_OK) return LA_ERR_INVALID_ARG;
+    PagedFillParams p;
+    p.c = make_paged(k_pages, v_pages, block_table, lens, B, Hkv, dqk, dv, num_pages, page_size, max_pages);
+    p.k = k;
+    p.v = v;
+    p.n_new = n_new;
+    p.pos = pos;
+    p.weights = weights;
+    p.positions = positions;
+    p.N = N;
+    p.vec_k = rows16(dqk, dtype);
+    p.vec_v = rows16(dv, dtype);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (dtype == LA_F32) return launch_pdl(paged_fill_kernel<float>, (int)blocks, kPagedFillThreads, 0, st, p);
+    return launch_pdl(paged_fill_kernel<__nv_bfloat16>, (int)blocks, kPagedFillThreads, 0, st, p);
+}
+
+size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
+                                       int with_weights, int dtype)
+{
+    (void)with_weights;
+    if (check_paged(B, Hq, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK) return 0;
+    return 0;
+}
+
+la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse, void *k_pages,
+                               void *v_pages, const int32_t *block_table, const int32_t *lens,
+                               const float *weights_in, float *weights_out, int32_t *positions, const int32_t *pos,
+                               void *workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int dqk, int dv,
+                               int num_pages, int page_size, int max_pages, int dtype, void *stream)
+{
+    const la_status sh = check_paged(B, Hq, Hkv, dqk, dv, num_pages, page_size, max_pages, dtype);
+    if (sh != LA_OK) return sh;
+    const la_status pt = check_paged_ptrs(k_pages, v_pages, block_table, lens);
+    if (pt != LA_OK) return pt;
+    if (!q || !y || (k == nullptr) != (v == nullptr) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(y, 16) || !aligned(lse, 4))
+        return LA_ERR_INVALID_ARG;
+    if ((weights_in == nullptr) != (weights_out == nullptr) || !aligned(weights_in, 4) || !aligned(weights_out, 4) ||
+        (positions == nullptr) != (pos == nullptr) || (positions && !k) || !aligned(positions, 4) || !aligned(pos, 4))
+        return LA_ERR_INVALID_ARG;
+    if (!same_or_apart(weights_in, weights_out, (size_t)B * Hkv * max_pages * page_size * sizeof(float)))
+        return LA_ERR_INVALID_ARG;
+    const size_t need = la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page_size, max_pages,
+                                                        weights_in != nullptr, dtype);
+    if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return LA_ERR_INVALID_ARG;
+    if (check_on_current_device(k_pages) != LA_OK) return LA_ERR_INVALID_ARG;
+    PagedDecodeParams p;
+    p.c = make_paged(k_pages, v_pages, block_table, lens, B, Hkv, dqk, dv, num_pages, page_size, max_pages);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.y = y;
+    p.lse = lse;
+    p.w_in = weights_in;
+    p.w_out = weights_out;
+    p.positions = positions;
+    p.pos = pos;
+    p.Hq = Hq;
+    p.scale = (float)(1.0 / sqrt((double)dqk));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (dtype == LA_F32) return launch_pdl(paged_decode_simple_kernel<float>, B * Hkv, kPagedThreads, 0, st, p);
+    return launch_pdl(paged_decode_simple_kernel<__nv_bfloat16>, B * Hkv, kPagedThreads, 0, st, p);
+}
+
+// Most slots that can move in one (b, h): as many as lie below the budget, or above it.
+static int64_t evict_maxmoves(int page_size, int max_pages, int budget)
+{
+    const int64_t above = (int64_t)max_pages * page_size - budget;
+    return above <= 0 ? 0 : above < budget ? above : budget;
+}
+
+size_t la_paged_evict_workspace_bytes(int B, int Hkv, int page_size, int max_pages, int budget)
+{
+    if (check_paged(B, Hkv, Hkv, 1, 1, 1, page_size, max_pages, LA_F32) != LA_OK || budget < 1) return 0;
+    // the slots that move, from and to; their number per (b, h); the new lengths
+    return ((size_t)B * Hkv * (2 * evict_maxmoves(page_size, max_pages, budget) + 1) + B) * sizeof(int);
+}
+
+la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_table, const int32_t *lens,
+                         int32_t *lens_out, const float *weights_in, float *weights_out, const int32_t *positions_in,
+                         int32_t *positions_out, const int32_t *pos, void *workspace, size_t workspace_bytes, int B,
+                         int Hkv, int dqk, int dv, int num_pages, int page_size, int max_pages, int budget,
+                         int recent, int dtype, void *stream)
+{
+    const la_status sh = check_paged(B, Hkv, Hkv, dqk, dv, num_pages, page_size, max_pages, dtype);
+    if (sh != LA_OK) return sh;
+    const la_status pt = check_paged_ptrs(k_pages, v_pages, block_table, lens);
+    if (pt != LA_OK) return pt;
+    if (budget < 1 || recent < 0 || recent > budget) return LA_ERR_INVALID_ARG;
+    if (!lens_out || !weights_in || !weights_out || !aligned(lens_out, 4) || !aligned(weights_in, 4) ||
+        !aligned(weights_out, 4) || (positions_in == nullptr) != (positions_out == nullptr) ||
+        !aligned(positions_in, 4) || !aligned(positions_out, 4) || !aligned(pos, 4))
+        return LA_ERR_INVALID_ARG;
+    if (recent > 0 && (!positions_in || !pos)) return LA_ERR_INVALID_ARG;
+    const size_t slots = (size_t)B * Hkv * max_pages * page_size;
+    if (!same_or_apart(weights_in, weights_out, slots * sizeof(float)) ||
+        !same_or_apart(positions_in, positions_out, slots * sizeof(int)) ||
+        !same_or_apart(lens, lens_out, (size_t)B * sizeof(int)))
+        return LA_ERR_INVALID_ARG;
+    const size_t need = la_paged_evict_workspace_bytes(B, Hkv, page_size, max_pages, budget);
+    if (workspace_bytes < need || !workspace || !aligned(workspace, 16)) return LA_ERR_INVALID_ARG;
+    if (check_on_current_device(k_pages) != LA_OK) return LA_ERR_INVALID_ARG;
+    PagedEvictParams p;
+    p.c = make_paged(k_pages, v_pages, block_table, lens, B, Hkv, dqk, dv, num_pages, page_size, max_pages);
+    p.lens_out = lens_out;
+    p.w_in = weights_in;
+    p.w_out = weights_out;
+    p.pos_in = positions_in;
+    p.pos_out = positions_out;
+    p.pos = pos;
+    p.budget = budget;
+    p.recent = recent;
+    p.maxmoves = (int)evict_maxmoves(page_size, max_pages, budget);
+    p.holes = (int *)workspace;
+    p.movers = p.holes + (size_t)B * Hkv * p.maxmoves;
+    p.count = p.movers + (size_t)B * Hkv * p.maxmoves;
+    p.newlen = p.count + (size_t)B * Hkv;
+    p.vec_k = rows16(dqk, dtype);
+    p.vec_v = rows16(dv, dtype);
+    cudaStream_t st = (cudaStream_t)stream;
+    const la_status s1 = launch_pdl(paged_evict_select_kernel, B * Hkv, kEvictThreads, 0, st, p);
+    if (s1 != LA_OK) return s1;
+    const int splits = 1;
+    if (dtype == LA_F32) return launch_pdl(paged_evict_move_kernel<float>, B * Hkv * splits, 256, 0, st, p, splits);
+    return launch_pdl(paged_evict_move_kernel<__nv_bfloat16>, B * Hkv * splits, 256, 0, st, p, splits);
+}
+
+int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
+                         int with_weights, int dtype, char *buf, size_t buflen)
+{
+    (void)with_weights;
+    if (op < 0 || op > 2 ||
+        check_paged(B, op == 1 ? Hq : Hkv, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK)
+        return -1;
+    const char *nm = op == 0   ? "paged_fill_kernel"
+                     : op == 1 ? "paged_decode_simple_kernel"
+                               : "paged_evict_select_kernel,paged_evict_move_kernel";
+    if (buf && buflen) {
+        strncpy(buf, nm, buflen - 1);
+        buf[buflen - 1] = 0;
+    }
+    return op == 2 ? 2 : 1;
 }
 
 la_status la_feature_map(const void *x, void *phi, int64_t rows, int dqk, int fmap, int dtype,

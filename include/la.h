@@ -322,6 +322,123 @@ LA_API la_status la_swa_decode_step(const void *q, const void *k, const void *v,
                                     void *k_cache, void *v_cache, const int32_t *pos,
                                     int B, int H, int dqk, int dv, int window, int dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A paged key/value cache for global softmax attention, the attention of one
+ * new token over it, and eviction by accumulated attention weight.
+ *
+ * The sliding-window cache above holds a fixed number of tokens.  This one
+ * grows: the tokens of a sequence lie in pages taken from a pool, so sequences
+ * of any length share one allocation.  The cache of one layer is
+ *   k_pages     [num_pages, Hkv, page_size, dqk] dtype, v_pages
+ *               [num_pages, Hkv, page_size, dv] dtype: the pool
+ *   block_table [B, max_pages] int32: slot t of sequence b lies in page
+ *               block_table[b, t / page_size], row t mod page_size, for every
+ *               head.  Only the entries of pages in use are read.
+ *   lens        [B] int32: slots held by each sequence (the same for its heads)
+ * and, for a cache that is kept within a budget, per (b, h) and slot
+ *   weights     [B, Hkv, max_pages * page_size] fp32: the attention weight the
+ *               token has received, summed over steps and query heads
+ *   positions   [B, Hkv, max_pages * page_size] int32: the token's position in
+ *               its sequence (after an eviction the heads hold different
+ *               tokens, in any order)
+ *   pos         [B] int32: tokens the sequence has seen so far (>= lens).
+ * All of these are DEVICE memory.  The caller allots pages and advances lens
+ * and pos.  A page may stand in several tables as long as it is only read;
+ * slots that a call writes must belong to one sequence.
+ *
+ * Sizes: dqk, dv in [1,128]; any page_size >= 1; num_pages * Hkv * page_size
+ * and max_pages * page_size below 2^31 (element offsets are 64 bits wide).
+ * What lies in device memory is checked there: a sequence with lens[b] < 0,
+ * more slots than its table holds, or pos[b] < 0 where pos is used, is left
+ * as it was (its outputs are not written either) and sets LA_ERR_DEVICE_CHECK
+ * in the device status word.  A block_table entry outside [0, num_pages) sets
+ * it too; its tokens are neither written nor, in a decode step, attended to,
+ * and la_paged_evict leaves the sequence as it was. */
+
+/* Append tokens to the cache: slot lens[b] + i takes k[b,h,i], v[b,h,i] for
+ * i < n_new[b].  The counterpart of la_swa_cache_fill: k, v [B,Hkv,N,*] dtype
+ * as a prefill has them.
+ *   n_new     [B] int32, nullable: tokens of each sequence in a padded batch,
+ *             0 <= n_new[b] <= N (checked on the device); null: N for all
+ *   weights   nullable: 0 is written for the new slots
+ *   positions nullable, with pos (both or neither): pos[b] + i is written
+ * lens and pos are read only. */
+LA_API la_status la_paged_cache_fill(const void *k, const void *v, void *k_pages, void *v_pages,
+                                     const int32_t *block_table, const int32_t *lens, const int32_t *n_new,
+                                     float *weights, int32_t *positions, const int32_t *pos,
+                                     int B, int Hkv, int N, int dqk, int dv, int num_pages, int page_size,
+                                     int max_pages, int dtype, void *stream);
+
+/* Bytes of device workspace la_paged_decode_step needs: the partial results of
+ * sequences that are split across thread blocks and, with_weights != 0, the
+ * scores of the step.  The rules of la_forward_workspace_bytes. */
+LA_API size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
+                                              int with_weights, int dtype);
+
+/* One decode step of softmax attention over the whole cache.  Query heads
+ * hq = h * (Hq / Hkv) .. share key/value head h:
+ *
+ *     y[b,hq] = sum_t p_t v_t,   p_t = softmax_t(s_t),   s_t = q[b,hq] . k_t / sqrt(dqk)
+ *
+ * over the n slots the sequence holds.  With k, v [B,Hkv,*] the new token is
+ * stored in slot lens[b] first and attended to (n = lens[b] + 1; the caller
+ * advances lens); with both null the step attends to the cache as it is
+ * (n = lens[b]: an encoder's states, a second query on the same cache).
+ *   q  [B,Hq,dqk] dtype, read; y [B,Hq,dv] dtype, written
+ *   lse [B,Hq] fp32 nullable: log sum_t exp(s_t)
+ *   weights_in, weights_out  [B,Hkv,max_pages*page_size] fp32, nullable (both
+ *      or neither; the same pointer, or not overlapping): for the n slots
+ *      weights_out[b,h,t] = weights_in[b,h,t] + the sum of p_t over the query
+ *      heads of h.  The new token's slot starts at 0, whatever weights_in holds.
+ *   positions nullable, with pos (both or neither) and only with k, v:
+ *      positions[b,h,lens[b]] = pos[b].
+ *   workspace at least la_paged_decode_workspace_bytes(...) bytes.
+ * n = 0 gives y = 0 and lse = -inf.  Slots past n are not read: what stale
+ * pages hold does not matter.
+ * Errors: LA_ERR_INVALID_ARG also when Hq is not a multiple of Hkv. */
+LA_API la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse,
+                                      void *k_pages, void *v_pages, const int32_t *block_table, const int32_t *lens,
+                                      const float *weights_in, float *weights_out, int32_t *positions,
+                                      const int32_t *pos, void *workspace, size_t workspace_bytes,
+                                      int B, int Hq, int Hkv, int dqk, int dv, int num_pages, int page_size,
+                                      int max_pages, int dtype, void *stream);
+
+/* Bytes of device workspace la_paged_evict needs (the slots that move); the
+ * rules of la_forward_workspace_bytes. */
+LA_API size_t la_paged_evict_workspace_bytes(int B, int Hkv, int page_size, int max_pages, int budget);
+
+/* Evict: every (b, h) with more than `budget` slots keeps `budget` of them,
+ * the others are dropped.  Kept are first the recent tokens, those with
+ * positions[b,h,t] >= pos[b] - recent, then the slots of largest weight; among
+ * equal weights the lowest slot (a NaN weight counts as -inf, and the same
+ * order decides when the recent tokens alone exceed the budget).
+ * The slots are then made contiguous in place: the kept slots at or above
+ * `budget`, in ascending order, move into the dropped slots below it, in
+ * ascending order.  The other kept slots stay where they are: softmax does
+ * not depend on the order of the slots, and only the moved rows cost traffic.
+ *   lens, lens_out  [B] int32: slots held before and after, min(lens[b],
+ *      budget).  lens_out may be lens.  The pages past lens_out are free.
+ *   weights_in, weights_out  fp32, required; positions_in, positions_out int32,
+ *      nullable (both or neither, required when recent > 0): entries
+ *      [0, lens_out[b]) of the outputs are written, following the moves.  An
+ *      output may be its input (in place); otherwise they must not overlap.
+ *   pos     [B] int32, required when recent > 0
+ *   budget >= 1, 0 <= recent <= budget
+ *   workspace at least la_paged_evict_workspace_bytes(...) bytes.
+ * A sequence with lens[b] <= budget keeps its slots (lens_out = lens). */
+LA_API la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_table, const int32_t *lens,
+                                int32_t *lens_out, const float *weights_in, float *weights_out,
+                                const int32_t *positions_in, int32_t *positions_out, const int32_t *pos,
+                                void *workspace, size_t workspace_bytes, int B, int Hkv, int dqk, int dv,
+                                int num_pages, int page_size, int max_pages, int budget, int recent, int dtype,
+                                void *stream);
+
+/* la_kernel_plan for the paged calls: op 0 = la_paged_cache_fill, 1 =
+ * la_paged_decode_step, 2 = la_paged_evict (Hq ignored in 0 and 2).  Same
+ * output rules. */
+LA_API int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
+                                int with_weights, int dtype, char *buf, size_t buflen);
+
 /* la_forward for callers that cannot allocate device memory.
  *
  * The pages have no counterpart to this entry point; it is an interface
