@@ -646,6 +646,118 @@ static la_status swa_simt_launch(const void *q, const void *k, const void *v, vo
     return launch_status();
 }
 
+// Sizes of the paged calls.  Rows are 32-bit indices, elements 64-bit offsets.
+static la_status check_paged(int B, int Hq, int Hkv, int dqk, int dv, int num_pages, int page_size, int max_pages,
+                             int dtype)
+{
+    if (B < 1 || Hq < 1 || Hkv < 1 || dqk < 1 || dv < 1 || num_pages < 1 || page_size < 1 || max_pages < 1)
+        return LA_ERR_INVALID_ARG;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (Hq % Hkv) return LA_ERR_INVALID_ARG;
+    const int64_t lim = (int64_t)1 << 31;
+    if ((int64_t)num_pages * Hkv >= lim || (int64_t)num_pages * Hkv * page_size >= lim) return LA_ERR_INVALID_ARG;
+    if ((int64_t)max_pages * page_size >= lim) return LA_ERR_INVALID_ARG;
+    if ((int64_t)B * Hq * (dqk > dv ? dqk : dv) >= lim) return LA_ERR_INVALID_ARG;
+    if (dqk > 128 || dv > 128) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+static PagedCache make_paged(void *kp, void *vp, const int32_t *table, const int32_t *lens, int B, int Hkv, int dqk,
+                             int dv, int num_pages, int page_size, int max_pages)
+{
+    PagedCache c;
+    c.kp = kp;
+    c.vp = vp;
+    c.table = table;
+    c.lens = lens;
+    c.B = B;
+    c.Hkv = Hkv;
+    c.dqk = dqk;
+    c.dv = dv;
+    c.num_pages = num_pages;
+    c.page = page_size;
+    c.max_pages = max_pages;
+    c.shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (page_size == 1 << i) c.shift = i;
+    return c;
+}
+
+static size_t elem_size(int dtype) { return dtype == LA_F32 ? 4 : 2; }
+static bool rows16(int d, int dtype) { return d * elem_size(dtype) % 16 == 0; }
+
+// The cache's own arguments, shared by the three calls.
+static la_status check_paged_ptrs(const void *kp, const void *vp, const int32_t *table, const int32_t *lens)
+{
+    if (!kp || !vp || !table || !lens) return LA_ERR_INVALID_ARG;
+    if (!aligned(kp, 16) || !aligned(vp, 16) || !aligned(table, 4) || !aligned(lens, 4)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+// How a decode step is cut up: units of at most 16 query heads, one range of
+// tiles per block.
+struct PagedPlan {
+    bool mma;
+    int nsub, gs, grid;
+    int64_t stride;   // slots per row of kept scores: whole tiles
+    size_t ml_off() const { return ((size_t)grid * sizeof(PagedRecord) + 15) / 16 * 16; }
+};
+
+static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages, int dtype,
+                            PagedPlan *pl)
+{
+    const int g = Hq / Hkv;
+    if (g > kPagedMaxGroup) return LA_ERR_UNSUPPORTED;
+    pl->mma = dtype == LA_BF16 && dqk % 8 == 0 && dv % 8 == 0;
+    pl->nsub = (g + kPagedRows - 1) / kPagedRows;
+    pl->gs = (g + pl->nsub - 1) / pl->nsub;
+    pl->grid = kNumSms * (pl->mma || (dqk <= 64 && dv <= 64) ? 2 : 1);
+    const int64_t tiles = ((int64_t)max_pages * page_size + kPagedTile - 1) / kPagedTile;
+    pl->stride = tiles * kPagedTile;
+    // a range's length and a unit's tiles are 32-bit
+    if ((int64_t)B * Hkv * pl->nsub >= (int64_t)1 << 31 || (double)tiles * B * Hkv * pl->nsub / pl->grid >= 2e9)
+        return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+template <int DQ, int DV, bool HI>
+static la_status paged_mma_run(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+{
+    using Cfg = PagedMma<DQ, DV, HI>;
+    if (set_smem<paged_decode_mma_kernel<DQ, DV, HI>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
+    return launch_pdl(paged_decode_mma_kernel<DQ, DV, HI>, pl.grid, kPagedThreads, Cfg::SMEM, st, p);
+}
+
+static la_status paged_mma(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+{
+    const bool hi = pl.gs > 8;
+    if (p.c.dqk <= 64) {
+        if (p.c.dv <= 64) return hi ? paged_mma_run<64, 64, true>(p, pl, st) : paged_mma_run<64, 64, false>(p, pl, st);
+        return hi ? paged_mma_run<64, 128, true>(p, pl, st) : paged_mma_run<64, 128, false>(p, pl, st);
+    }
+    if (p.c.dv <= 64) return hi ? paged_mma_run<128, 64, true>(p, pl, st) : paged_mma_run<128, 64, false>(p, pl, st);
+    return hi ? paged_mma_run<128, 128, true>(p, pl, st) : paged_mma_run<128, 128, false>(p, pl, st);
+}
+
+template <typename T, int D, int GM>
+static la_status paged_simt_run(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+{
+    using Cfg = PagedSimt<T, D, GM>;
+    if (set_smem<paged_decode_simt_kernel<T, D, GM>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
+    return launch_pdl(paged_decode_simt_kernel<T, D, GM>, pl.grid, kPagedThreads, Cfg::SMEM, st, p);
+}
+
+template <typename T>
+static la_status paged_simt(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+{
+    if (p.c.dqk <= 64 && p.c.dv <= 64) {
+        if (pl.gs == 1) return paged_simt_run<T, 64, 1>(p, pl, st);
+        return pl.gs <= 4 ? paged_simt_run<T, 64, 4>(p, pl, st) : paged_simt_run<T, 64, 16>(p, pl, st);
+    }
+    if (pl.gs == 1) return paged_simt_run<T, 128, 1>(p, pl, st);
+    return pl.gs <= 4 ? paged_simt_run<T, 128, 4>(p, pl, st) : paged_simt_run<T, 128, 16>(p, pl, st);
+}
+
 extern "C" {
 
 int la_version(void) { return 100; }
@@ -747,54 +859,6 @@ static bool overlaps(const void *a, size_t na, const void *b, size_t nb)
     if (!a || !b) return false;
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return x < y + nb && y < x + na;
-}
-
-// Sizes of the paged calls.  Rows are 32-bit indices, elements 64-bit offsets.
-static la_status check_paged(int B, int Hq, int Hkv, int dqk, int dv, int num_pages, int page_size, int max_pages,
-                             int dtype)
-{
-    if (B < 1 || Hq < 1 || Hkv < 1 || dqk < 1 || dv < 1 || num_pages < 1 || page_size < 1 || max_pages < 1)
-        return LA_ERR_INVALID_ARG;
-    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
-    if (Hq % Hkv) return LA_ERR_INVALID_ARG;
-    const int64_t lim = (int64_t)1 << 31;
-    if ((int64_t)num_pages * Hkv >= lim || (int64_t)num_pages * Hkv * page_size >= lim) return LA_ERR_INVALID_ARG;
-    if ((int64_t)max_pages * page_size >= lim) return LA_ERR_INVALID_ARG;
-    if ((int64_t)B * Hq * (dqk > dv ? dqk : dv) >= lim) return LA_ERR_INVALID_ARG;
-    if (dqk > 128 || dv > 128) return LA_ERR_UNSUPPORTED;
-    return LA_OK;
-}
-
-static PagedCache make_paged(void *kp, void *vp, const int32_t *table, const int32_t *lens, int B, int Hkv, int dqk,
-                             int dv, int num_pages, int page_size, int max_pages)
-{
-    PagedCache c;
-    c.kp = kp;
-    c.vp = vp;
-    c.table = table;
-    c.lens = lens;
-    c.B = B;
-    c.Hkv = Hkv;
-    c.dqk = dqk;
-    c.dv = dv;
-    c.num_pages = num_pages;
-    c.page = page_size;
-    c.max_pages = max_pages;
-    c.shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (page_size == 1 << i) c.shift = i;
-    return c;
-}
-
-static size_t elem_size(int dtype) { return dtype == LA_F32 ? 4 : 2; }
-static bool rows16(int d, int dtype) { return d * elem_size(dtype) % 16 == 0; }
-
-// The cache's own arguments, shared by the three calls.
-static la_status check_paged_ptrs(const void *kp, const void *vp, const int32_t *table, const int32_t *lens)
-{
-    if (!kp || !vp || !table || !lens) return LA_ERR_INVALID_ARG;
-    if (!aligned(kp, 16) || !aligned(vp, 16) || !aligned(table, 4) || !aligned(lens, 4)) return LA_ERR_INVALID_ARG;
-    return LA_OK;
 }
 
 // An input and output of the same size: one buffer, or two that do not overlap.
@@ -1186,9 +1250,13 @@ la_status la_paged_cache_fill(const void *k, const void *v, void *k_pages, void 
 size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
                                        int with_weights, int dtype)
 {
-    (void)with_weights;
-    if (check_paged(B, Hq, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK) return 0;
-    return 0;
+    PagedPlan pl;
+    if (check_paged(B, Hq, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK ||
+        paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl) != LA_OK)
+        return 0;
+    size_t bytes = pl.ml_off() + (size_t)pl.grid * 2 * kPagedRows * (sizeof(float2) + dv * sizeof(float));
+    if (with_weights) bytes += (size_t)B * Hq * (pl.stride + 2) * sizeof(float);
+    return bytes;
 }
 
 la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse, void *k_pages,
@@ -1209,9 +1277,12 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
         return LA_ERR_INVALID_ARG;
     if (!same_or_apart(weights_in, weights_out, (size_t)B * Hkv * max_pages * page_size * sizeof(float)))
         return LA_ERR_INVALID_ARG;
+    PagedPlan pl;
+    const la_status ps = paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl);
+    if (ps != LA_OK) return ps;
     const size_t need = la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page_size, max_pages,
                                                         weights_in != nullptr, dtype);
-    if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return LA_ERR_INVALID_ARG;
+    if (workspace_bytes < need || !workspace || !aligned(workspace, 16)) return LA_ERR_INVALID_ARG;
     if (check_on_current_device(k_pages) != LA_OK) return LA_ERR_INVALID_ARG;
     PagedDecodeParams p;
     p.c = make_paged(k_pages, v_pages, block_table, lens, B, Hkv, dqk, dv, num_pages, page_size, max_pages);
@@ -1225,10 +1296,26 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
     p.positions = positions;
     p.pos = pos;
     p.Hq = Hq;
-    p.scale = (float)(1.0 / sqrt((double)dqk));
+    p.g = Hq / Hkv;
+    p.nsub = pl.nsub;
+    p.gs = pl.gs;
+    p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)dqk));
+    p.vec = rows16(dqk, dtype) && rows16(dv, dtype);
+    uint8_t *ws = (uint8_t *)workspace;
+    p.rec = (PagedRecord *)ws;
+    p.ml = (float2 *)(ws + pl.ml_off());
+    p.part = (float *)(p.ml + (size_t)pl.grid * 2 * kPagedRows);
+    float *more = p.part + (size_t)pl.grid * 2 * kPagedRows * dv;
+    p.stride = pl.stride;
+    // (an even number of floats ahead of the scores keeps their rows 8-byte aligned)
+    p.lse2 = weights_in ? more : nullptr;
+    p.scores = weights_in ? more + ((size_t)B * Hq + 1) / 2 * 2 : nullptr;
     cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == LA_F32) return launch_pdl(paged_decode_simple_kernel<float>, B * Hkv, kPagedThreads, 0, st, p);
-    return launch_pdl(paged_decode_simple_kernel<__nv_bfloat16>, B * Hkv, kPagedThreads, 0, st, p);
+    const la_status s1 = pl.mma ? paged_mma(p, pl, st)
+                         : dtype == LA_F32 ? paged_simt<float>(p, pl, st) : paged_simt<__nv_bfloat16>(p, pl, st);
+    if (s1 != LA_OK) return s1;
+    if (dtype == LA_F32) return launch_pdl(paged_join_kernel<float>, pl.grid, kPagedThreads, 0, st, p);
+    return launch_pdl(paged_join_kernel<__nv_bfloat16>, pl.grid, kPagedThreads, 0, st, p);
 }
 
 // Most slots that can move in one (b, h): as many as lie below the budget, or above it.
@@ -1301,14 +1388,17 @@ int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int pa
     if (op < 0 || op > 2 ||
         check_paged(B, op == 1 ? Hq : Hkv, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK)
         return -1;
+    PagedPlan pl;
+    if (op == 1 && paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl) != LA_OK) return -1;
     const char *nm = op == 0   ? "paged_fill_kernel"
-                     : op == 1 ? "paged_decode_simple_kernel"
-                               : "paged_evict_select_kernel,paged_evict_move_kernel";
+                     : op == 2 ? "paged_evict_select_kernel,paged_evict_move_kernel"
+                     : pl.mma  ? "paged_decode_mma_kernel,paged_join_kernel"
+                               : "paged_decode_simt_kernel,paged_join_kernel";
     if (buf && buflen) {
         strncpy(buf, nm, buflen - 1);
         buf[buflen - 1] = 0;
     }
-    return op == 2 ? 2 : 1;
+    return op == 0 ? 1 : 2;
 }
 
 la_status la_feature_map(const void *x, void *phi, int64_t rows, int dqk, int fmap, int dtype,

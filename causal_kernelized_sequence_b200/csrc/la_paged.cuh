@@ -98,6 +98,39 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 }
 
 // ------------------------------------------------------- one-token attention
+//
+// For every sequence b and key/value head h, up to 16 query heads that share
+// the head form a unit (groups of more than 16 heads are several units), and a
+// unit's slots are cut into tiles of 64.  All tiles of the call, in (b, h, tile)
+// order, are dealt out in equal contiguous ranges, one per block: one long
+// sequence or many ragged ones load every SM alike, and each block finds its
+// range from lens by one scan.  Inside a tile each of the four warps owns 16
+// slots, with its own running maximum, sum and accumulators, so warps meet only
+// where a unit ends.  A unit inside one range is finished there; the parts of
+// one that crosses ranges go to the workspace and the join kernel adds them,
+// in the order of the ranges:  with M = max m_i,
+//     y = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i      (scores in log2 units).
+// The same launch then adds the normalised weights, from the step's scores
+// kept in the workspace: a weight needs the whole row's sum.
+
+constexpr int kPagedThreads = 128;
+constexpr int kPagedWarps = kPagedThreads / 32;
+constexpr int kPagedTile = 64;
+constexpr int kPagedRows = 16;       // query heads of a unit
+constexpr int kPagedMaxGroup = 128;  // query heads per key/value head
+
+// A unit that crosses ranges, as the join needs it: tiles [first, end) of all.
+struct PagedSpan {
+    long long first, end;
+    int b, u;   // b < 0: none
+};
+// What a block of the decode kernel leaves for the block of the join: where
+// its range starts, and the units it shares with the ranges before and after.
+struct PagedRecord {
+    PagedSpan head, tail;
+    int b, u, tile, tiles;   // start of the range, and its length (0: idle)
+    long long chunk;         // tiles per range
+};
 
 struct PagedDecodeParams {
     PagedCache c;
@@ -108,99 +141,866 @@ struct PagedDecodeParams {
     float *w_out;
     int *positions;
     const int *pos;
-    int Hq;
-    float scale;
+    int Hq, g, nsub, gs;     // query heads; per key/value head; units per head; heads per unit
+    float scale_log2;        // log2(e) / sqrt(dqk)
+    bool vec;                // rows start on 16-byte boundaries
+    PagedRecord *rec;        // [grid]
+    float2 *ml;              // [grid][2][16]: running maximum and sum of the head and tail parts
+    float *part;             // [grid][2][16][dv]: their accumulators
+    float *lse2;             // [B * Hq]: log2 of the sum of exponentials (with weights)
+    float *scores;           // [B * Hq][stride]: the scores in log2 units (with weights)
+    long long stride;
 };
 
-constexpr int kPagedThreads = 128;
-
-template <int NT>
-__device__ __forceinline__ float block_reduce(float x, bool is_max, float *red)
+// Slots that sequence b attends to, or -1 if its length or position is bad.
+__device__ __forceinline__ int paged_count(const PagedDecodeParams &p, int b)
 {
+    const int len = p.c.lens[b], more = p.k ? 1 : 0;
+    if (len < 0 || len > p.c.cap() - more || (p.pos && p.pos[b] < 0)) return -1;
+    return len + more;
+}
+__device__ __forceinline__ int paged_tiles(int n) { return n <= 0 ? 1 : (n + kPagedTile - 1) / kPagedTile; }
+
+// Exclusive prefix of x over the block in thread order, and the total.
+template <int NT, typename I>
+__device__ __forceinline__ I block_scan(I x, I *part, I &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    I s = x;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, x, off);
-        x = is_max ? fmaxf(x, o) : x + o;
+    for (int off = 1; off < 32; off <<= 1) {
+        const I o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
     }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    if (lane == 31) part[warp] = s;
     __syncthreads();
-    x = red[0];
+    I before = 0;
+    total = 0;
 #pragma unroll
-    for (int i = 1; i < NT / 32; ++i) x = is_max ? fmaxf(x, red[i]) : x + red[i];
-    return x;
+    for (int i = 0; i < NT / 32; ++i) {
+        if (i < warp) before += part[i];
+        total += part[i];
+    }
+    return before + s - x;
 }
 
-// One block per (b, key/value head): for each query head a pass over the cache
-// in tiles of 128 tokens with the running maximum and sum, then, if weights
-// are kept, a second one that adds the normalised weights.
+// A position in the (b, unit, tile) order.
+struct PagedWalk {
+    int b, u, tile, nt, n;
+    __device__ __forceinline__ void load(const PagedDecodeParams &p)
+    {
+        n = paged_count(p, b);
+        nt = paged_tiles(n);
+    }
+    // to the next tile (not past the last sequence)
+    __device__ __forceinline__ void next(const PagedDecodeParams &p)
+    {
+        if (++tile < nt) return;
+        tile = 0;
+        if (++u < p.c.Hkv * p.nsub) return;
+        u = 0;
+        ++b;
+        load(p);
+    }
+};
+
+// This block's range: sets the walk to its start and returns its number of tiles.
+__device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk &w, long long &first, long long &chunk)
+{
+    __shared__ long long part[kPagedWarps], found[2];
+    const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
+    const int slab = (B + kPagedThreads - 1) / kPagedThreads, b0 = min(B, tid * slab), b1 = min(B, b0 + slab);
+    long long mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += paged_tiles(paged_count(p, b));
+    long long before = block_scan<kPagedThreads>(mine, part, total);
+    total *= U;
+    chunk = (total + gridDim.x - 1) / gridDim.x;
+    first = blockIdx.x * chunk;
+    const long long x = first / U;
+    if (first < total && x >= before && x < before + mine) {
+        int b = b0;
+        for (;; ++b) {
+            const int nt = paged_tiles(paged_count(p, b));
+            if (x < before + nt) break;
+            before += nt;
+        }
+        found[0] = b;
+        found[1] = before;
+    }
+    __syncthreads();
+    if (first >= total) return 0;
+    w.b = (int)found[0];
+    w.load(p);
+    const long long off = first - U * found[1];   // below U * nt
+    w.u = (int)(off / w.nt);
+    w.tile = (int)(off - (long long)w.u * w.nt);
+    return (int)(total - first < chunk ? total - first : chunk);
+}
+
+// Records of a range for the join, written by thread 0 of the decode kernel.
+__device__ __forceinline__ void paged_record(const PagedDecodeParams &p, const PagedWalk &w, int tiles,
+                                             long long chunk)
+{
+    PagedRecord &r = p.rec[blockIdx.x];
+    r.head.b = r.tail.b = -1;
+    r.tiles = tiles;
+    r.chunk = chunk;
+    r.b = w.b;
+    r.u = w.u;
+    r.tile = w.tile;
+}
+
+// Where one unit's part of a range ends: the four warps' rows r0 .. r0 + 7 lie
+// in obuf [warp][8][DV] and their maxima and sums in mls [warp][16].  Finishes
+// the rows (`whole`) or leaves them to the join as part `slot`.
+template <typename T, int DV>
+__device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const PagedWalk &w, const float *obuf,
+                                            const float2 *mls, int r0, int rows, bool whole, int slot)
+{
+    const int tid = threadIdx.x, col = tid % DV;
+    const size_t hq0 = (size_t)w.b * p.Hq + (w.u / p.nsub) * p.g + (w.u % p.nsub) * p.gs;
+    for (int r = tid / DV; r < 8 && r0 + r < rows; r += kPagedThreads / DV) {
+        float M = -INFINITY, L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPagedWarps; ++i) M = fmaxf(M, mls[i * kPagedRows + r0 + r].x);
+        const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int i = 0; i < kPagedWarps; ++i) {
+            const float2 e = mls[i * kPagedRows + r0 + r];
+            const float f = exp2f(e.x - base);
+            L = fmaf(f, e.y, L);
+            acc = fmaf(f, obuf[(i * 8 + r) * DV + col], acc);
+        }
+        if (whole) {
+            const bool none = L == 0.f;   // nothing to attend to
+            if (col < p.c.dv) st((T *)p.y + (hq0 + r0 + r) * p.c.dv + col, none ? 0.f : acc / L);
+            if (col == 0) {
+                if (p.lse) p.lse[hq0 + r0 + r] = none ? -INFINITY : M * 0.693147180559945309f + logf(L);
+                if (p.lse2) p.lse2[hq0 + r0 + r] = none ? -INFINITY : M + log2f(L);
+            }
+        } else {
+            const size_t at = ((size_t)blockIdx.x * 2 + slot) * kPagedRows + r0 + r;
+            if (col < p.c.dv) p.part[at * p.c.dv + col] = acc;
+            if (col == 0) p.ml[at] = make_float2(M, L);
+        }
+    }
+}
+
+// The new token of the unit's sequence goes to its slot (once per head).
 template <typename T>
-__global__ void __launch_bounds__(kPagedThreads) paged_decode_simple_kernel(const PagedDecodeParams p)
+__device__ __forceinline__ void paged_store_new(const PagedDecodeParams &p, const PagedWalk &w)
+{
+    const PagedCache &c = p.c;
+    const int h = w.u / p.nsub, t = w.n - 1, row = paged_row(c, w.b, h, t), tid = threadIdx.x;
+    const size_t bh = (size_t)w.b * c.Hkv + h;
+    if (row < 0) return;
+    for (int i = tid; i < c.dqk; i += kPagedThreads) ((T *)c.kp)[(size_t)row * c.dqk + i] = ((const T *)p.k)[bh * c.dqk + i];
+    for (int i = tid; i < c.dv; i += kPagedThreads) ((T *)c.vp)[(size_t)row * c.dv + i] = ((const T *)p.v)[bh * c.dv + i];
+    if (p.positions && tid == 0) p.positions[bh * c.cap() + t] = p.pos[w.b];
+}
+
+// The end of a unit's part [t0, w.tile] of a range: whether it is whole, and
+// what the join has to know if it is not.  Returns the slot of the part.
+__device__ __forceinline__ int paged_part(const PagedDecodeParams &p, const PagedWalk &w, int t0, long long at,
+                                          bool &whole)
+{
+    whole = t0 == 0 && w.tile == w.nt - 1;
+    if (whole) return 0;
+    const int slot = t0 == 0 ? 1 : 0;
+    if (threadIdx.x == 0) {
+        PagedSpan &s = slot ? p.rec[blockIdx.x].tail : p.rec[blockIdx.x].head;
+        s.first = at - w.tile;
+        s.end = s.first + w.nt;
+        s.b = w.b;
+        s.u = w.u;
+    }
+    return slot;
+}
+
+constexpr int kPagedNone = -1, kPagedNew = -2;   // rows that are not in the pool
+
+// Row of slot t0 + lane (lanes 0..15) of the walk's unit: kPagedNone past the
+// end or on a bad page, kPagedNew for the new token, which is read from the
+// caller's k, v.  `page` is the table's entry, fetched earlier.
+__device__ __forceinline__ int paged_entry(const PagedDecodeParams &p, const PagedWalk &w, int warp, int lane)
+{
+    const int t = w.tile * kPagedTile + warp * 16 + lane;
+    if (lane >= 16 || t >= w.n) return -1;
+    return p.c.table[(size_t)w.b * p.c.max_pages + (p.c.shift >= 0 ? t >> p.c.shift : t / p.c.page)];
+}
+__device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const PagedWalk &w, int warp, int lane, int page)
+{
+    const PagedCache &c = p.c;
+    const int t = w.tile * kPagedTile + warp * 16 + lane;
+    if (lane >= 16 || t >= w.n) return kPagedNone;
+    if ((unsigned)page >= (unsigned)c.num_pages) {
+        report(kStatusCheck);
+        return kPagedNone;
+    }
+    if (p.k && t == w.n - 1) return kPagedNew;
+    const int off = c.shift >= 0 ? t & (c.page - 1) : t % c.page;
+    return (page * c.Hkv + w.u / p.nsub) * c.page + off;
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// D += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// What bf16x2(lo, hi) rounded off, as bf16 again.
+__device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
+{
+    return bf16x2(lo - __uint_as_float(r << 16), hi - __uint_as_float(r & 0xffff0000u));
+}
+
+// bf16, dqk and dv multiples of 8, on the tensor cores with mma.sync: the work
+// per byte (2 * heads FLOP) is far below what a tcgen05 tile is for, and its 16
+// rows hold the query heads.  Operands go from global memory to the registers
+// of the thread that needs them, through 16-byte slots of shared memory that
+// only this thread writes and reads (cp.async, `ST` tiles deep), so nothing but
+// the wait for its own copies orders a warp.  No transpose is needed, because
+// a sum does not depend on the order of its terms and a matrix product not on
+// the order of its columns:
+//   S = Q K^T  thread (r = lane / 4, c = lane % 4) holds 8 consecutive
+//       coordinates 32 j + 8 c .. + 7 of key r (and r + 8): the two k-steps
+//       2j, 2j + 1 take them as their coordinates 2c, 2c+1, 2c+8, 2c+9; Q is
+//       held in the same order.
+//   O = P V    thread (r, c) holds the values 64 j + 8 r .. + 7 of the slots
+//       2c, 2c+1, 2c+8, 2c+9: a byte permutation pairs two slots, and column
+//       block e of the product is the values 64 j + 8 r + e.
+// P enters as two bf16 halves, p = hi + lo (error 2^-17 of p instead of 2^-9).
+// With at most 8 heads (HI false) the low half takes the rows 8..15, which are
+// free, and costs no further MMA.
+template <int DQ, int DV, bool HI>
+struct PagedMma {
+    static constexpr int KP = DQ / 16, VP = DV / 16;           // 16-byte pieces per thread and tile
+    static constexpr int STAGE = (KP + VP) * 16 * kPagedThreads;
+    static constexpr int ST = DQ + DV > 128 ? 3 : 4;
+    static constexpr int OFF_O = ST * STAGE;
+    static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * DV * 4;
+    static constexpr int OFF_MASK = OFF_ML + kPagedWarps * kPagedRows * 8;
+    static constexpr int SMEM = OFF_MASK + kPagedWarps * ST * 4;
+    static constexpr int BLOCKS = 2;                           // per SM
+};
+
+template <int DQ, int DV, bool HI>
+__global__ void __launch_bounds__(kPagedThreads, PagedMma<DQ, DV, HI>::BLOCKS)
+paged_decode_mma_kernel(const PagedDecodeParams p)
+{
+    using Cfg = PagedMma<DQ, DV, HI>;
+    using T = __nv_bfloat16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    sm100::grid_dependency_wait();
+    sm100::launch_dependents();
+    const PagedCache &c = p.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
+    float *obuf = reinterpret_cast<float *>(smem + Cfg::OFF_O);
+    float2 *mls = reinterpret_cast<float2 *>(smem + Cfg::OFF_ML);
+    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MASK) + warp * Cfg::ST;
+    const uint32_t ring = sm100::smem_addr(smem) + tid * 16;
+
+    PagedWalk w;
+    long long at, chunk;
+    const int tiles = paged_range(p, w, at, chunk);
+    if (tid == 0) paged_record(p, w, tiles, chunk);
+    if (!tiles) return;
+    __syncthreads();   // the record is written before paged_part adds to it
+
+    // loads: `lw` is the tile whose loads are next, `page` its table entries
+    PagedWalk lw = w;
+    int issued = 0, page = paged_entry(p, lw, warp, lane);
+    auto issue = [&]() {
+        if (issued < tiles) {
+            const int stage = issued % Cfg::ST, h = lw.u / p.nsub;
+            const int row = paged_entry_row(p, lw, warp, lane, page);
+            const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);
+            if (lane == 0) masks[stage] = mask;
+            if (mask) {
+                const size_t bh = (size_t)lw.b * c.Hkv + h;
+                const uint32_t dst = ring + stage * Cfg::STAGE;
+                const T *kn = (const T *)p.k + bh * c.dqk, *vn = (const T *)p.v + bh * c.dv;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rw = __shfl_sync(0xffffffffu, row, i * 8 + r);
+                    const T *src = rw == kPagedNew ? kn : (const T *)c.kp + (size_t)max(rw, 0) * c.dqk;
+#pragma unroll
+                    for (int j = 0; j < DQ / 32; ++j) {
+                        const int col = j * 32 + cq * 8;
+                        const bool ok = rw != kPagedNone && col < c.dqk;
+                        cp_async16(dst + (i * (DQ / 32) + j) * (16 * kPagedThreads), ok ? src + col : src, ok);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rw = __shfl_sync(0xffffffffu, row, 2 * cq + (i & 1) + (i >> 1) * 8);
+                    const T *src = rw == kPagedNew ? vn : (const T *)c.vp + (size_t)max(rw, 0) * c.dv;
+#pragma unroll
+                    for (int j = 0; j < DV / 64; ++j) {
+                        const int col = j * 64 + r * 8;
+                        const bool ok = rw != kPagedNone && col < c.dv;
+                        cp_async16(dst + (Cfg::KP + j * 4 + i) * (16 * kPagedThreads), ok ? src + col : src, ok);
+                    }
+                }
+            }
+            if (++issued < tiles) {
+                lw.next(p);
+                page = paged_entry(p, lw, warp, lane);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < Cfg::ST - 1; ++s) issue();
+
+    constexpr int NR = HI ? 2 : 1;   // rows of a thread: r and r + 8
+    uint4 qf[DQ / 32][NR];
+    float o[DV / 8][4], m[NR], l[NR];
+    int t0 = 0;
+    for (int it = 0; it < tiles; ++it) {
+        const int h = w.u / p.nsub, sub = w.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
+        const size_t hq0 = (size_t)w.b * p.Hq + h * p.g + sub * p.gs;
+        if (it == 0 || w.tile == 0) {   // a new unit
+            t0 = w.tile;
+#pragma unroll
+            for (int j = 0; j < DQ / 32; ++j)
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const int col = j * 32 + cq * 8, row = r + 8 * i;
+                    qf[j][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < rows && col < c.dqk)
+                        qf[j][i] = *reinterpret_cast<const uint4 *>((const T *)p.q + (hq0 + row) * c.dqk + col);
+                }
+#pragma unroll
+            for (int i = 0; i < DV / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+        }
+        cp_async_wait<Cfg::ST - 2>();
+        __syncwarp();
+        const int stage = it % Cfg::ST;
+        const uint32_t mask = masks[stage];
+        issue();   // into the stage of the tile before, which every lane has used
+        if (mask) {
+            const uint32_t src = ring + stage * Cfg::STAGE;
+            float s[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < DQ / 32; ++j) {
+                    const uint4 kk = lds128(src + (i * (DQ / 32) + j) * (16 * kPagedThreads));
+                    const uint4 a = qf[j][0], b = HI ? qf[j][NR - 1] : make_uint4(0u, 0u, 0u, 0u);
+                    mma_16816(s[i], a.x, b.x, a.y, b.y, kk.x, kk.y);
+                    mma_16816(s[i], a.z, b.z, a.w, b.w, kk.z, kk.w);
+                }
+            }
+            // scores in log2 units; slot of s[i][e] (and s[i][e + 2]): 8 i + 2 cq + e
+            float mn[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                mn[n] = m[n];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[i][n * 2 + e];
+                        x = mask >> (8 * i + 2 * cq + e) & 1 ? x * p.scale_log2 : -INFINITY;
+                        mn[n] = fmaxf(mn[n], x);
+                    }
+                mn[n] = fmaxf(mn[n], __shfl_xor_sync(0xffffffffu, mn[n], 1));
+                mn[n] = fmaxf(mn[n], __shfl_xor_sync(0xffffffffu, mn[n], 2));
+                if (p.scores && r + 8 * n < rows) {
+                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16 + 2 * cq;
+                    *reinterpret_cast<float2 *>(to) = make_float2(s[0][n * 2], s[0][n * 2 + 1]);
+                    *reinterpret_cast<float2 *>(to + 8) = make_float2(s[1][n * 2], s[1][n * 2 + 1]);
+                }
+            }
+            bool grew = mn[0] != m[0];
+            if (HI) grew |= mn[NR - 1] != m[NR - 1];
+            if (__any_sync(0xffffffffu, grew)) {
+                float al[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    al[n] = exp2f(m[n] - (mn[n] == -INFINITY ? 0.f : mn[n]));
+                    l[n] *= al[n];
+                    m[n] = mn[n];
+                }
+#pragma unroll
+                for (int i = 0; i < DV / 8; ++i) {
+                    o[i][0] *= al[0];
+                    o[i][1] *= al[0];
+                    o[i][2] *= al[NR - 1];
+                    o[i][3] *= al[NR - 1];
+                }
+            }
+            uint32_t hi[2][NR], lo[2][NR];   // [slots 2cq.. / 2cq + 8..][row]
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const float base = m[n] == -INFINITY ? 0.f : m[n];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float e0 = exp2f(s[i][n * 2] - base), e1 = exp2f(s[i][n * 2 + 1] - base);
+                    l[n] += e0 + e1;
+                    hi[i][n] = bf16x2(e0, e1);
+                    lo[i][n] = bf16x2_rest(e0, e1, hi[i][n]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < DV / 64; ++j) {
+                if (j * 64 >= c.dv) break;
+                uint4 vv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vv[i] = lds128(src + (Cfg::KP + j * 4 + i) * (16 * kPagedThreads));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
+                    const uint32_t b0 = __byte_perm(word(vv[0], e / 2), word(vv[1], e / 2), sel);
+                    const uint32_t b1 = __byte_perm(word(vv[2], e / 2), word(vv[3], e / 2), sel);
+                    if (HI) {
+                        mma_16816(o[j * 8 + e], hi[0][0], hi[0][NR - 1], hi[1][0], hi[1][NR - 1], b0, b1);
+                        mma_16816(o[j * 8 + e], lo[0][0], lo[0][NR - 1], lo[1][0], lo[1][NR - 1], b0, b1);
+                    } else {
+                        mma_16816(o[j * 8 + e], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b0, b1);
+                    }
+                }
+            }
+        } else if (p.scores && w.n > 0) {   // slots past the end, or on bad pages: no weight
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                if (r + 8 * n < rows) {
+                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16 + 2 * cq;
+                    *reinterpret_cast<float2 *>(to) = make_float2(-INFINITY, -INFINITY);
+                    *reinterpret_cast<float2 *>(to + 8) = make_float2(-INFINITY, -INFINITY);
+                }
+        }
+        if (w.tile == w.nt - 1 || it == tiles - 1) {   // the unit, or its part in this range, ends
+            bool whole;
+            const int slot = paged_part(p, w, t0, at + it, whole);
+            if (w.n < 0) {
+                if (w.u == 0 && tid == 0) report(kStatusCheck);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+                    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+                    if (cq == 0) mls[warp * kPagedRows + r + 8 * n] = make_float2(m[n], l[n]);
+                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    float4 *to = reinterpret_cast<float4 *>(obuf + (warp * 8 + r) * DV + cq * 16);
+#pragma unroll
+                    for (int j = 0; j < DV / 64; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) {
+                                float x[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float *oo = o[j * 8 + f * 4 + i];
+                                    x[i] = HI ? oo[n * 2 + e] : oo[e] + oo[e + 2];
+                                }
+                                to[j * 16 + e * 2 + f] = make_float4(x[0], x[1], x[2], x[3]);
+                            }
+                    __syncthreads();
+                    paged_merge<T, DV>(p, w, obuf, mls, 8 * n, rows, whole, slot);
+                    __syncthreads();
+                }
+                if (p.k && sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
+            }
+        }
+        if (it < tiles - 1) w.next(p);
+    }
+    cp_async_wait<0>();
+}
+
+// fp32, and bf16 rows that do not start on 16-byte boundaries: the same walk
+// with fp32 FMA.  A quad of lanes shares a slot in the scores (lane c holds the
+// coordinates 16 j + 4 c .. + 3 of slots r and r + 8), and a lane owns four
+// columns of the output.  Rows reach the thread that uses them through its own
+// 16-byte slots of shared memory as above, as four floats each.
+template <typename T, int D, int GM>
+struct PagedSimt {
+    static constexpr int KP = D / 8;                 // pieces per thread and tile: 2 slots x D / 16
+    static constexpr int LR = D / 4, TP = 32 / LR;   // lanes per value row, rows per pass
+    static constexpr int VP = 16 / TP;
+    static constexpr int STAGE = (KP + VP) * 16 * kPagedThreads;
+    static constexpr int ST = D > 64 ? 2 : 3;
+    static constexpr int OFF_O = ST * STAGE;
+    static constexpr int OFF_Q = OFF_O + kPagedWarps * 8 * D * 4;          // [16][D] queries, shared by the warps
+    static constexpr int OFF_P = OFF_Q + GM * D * 4;                       // [warp][16][GM] weights
+    static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
+    static constexpr int OFF_MASK = OFF_ML + kPagedWarps * kPagedRows * 8;
+    static constexpr int SMEM = OFF_MASK + kPagedWarps * ST * 4;
+    static constexpr int BLOCKS = D > 64 ? 1 : 2;
+};
+
+// Four elements of a row (those below d; zeros after) into a 16-byte slot.
+template <typename T>
+__device__ __forceinline__ void paged_load4(uint32_t dst, const T *row, int col, int d, bool live, bool vec)
+{
+    if constexpr (sizeof(T) == 4) {
+        if (vec) {
+            const bool ok = live && col < d;
+            cp_async16(dst, ok ? row + col : row, ok);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool ok = live && col + e < d;
+                cp_async4(dst + 4 * e, ok ? row + col + e : row, ok);
+            }
+        }
+    } else {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = live && col + e < d ? ld(row + col + e) : 0.f;
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
+                     : "memory");
+    }
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a)
+{
+    const uint4 v = lds128(a);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+template <typename T, int D, int GM>
+__global__ void __launch_bounds__(kPagedThreads, PagedSimt<T, D, GM>::BLOCKS)
+paged_decode_simt_kernel(const PagedDecodeParams p)
+{
+    using Cfg = PagedSimt<T, D, GM>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    sm100::grid_dependency_wait();
+    sm100::launch_dependents();
+    const PagedCache &c = p.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
+    const int vcol = (lane % Cfg::LR) * 4, vrow = lane / Cfg::LR;
+    float *obuf = reinterpret_cast<float *>(smem + Cfg::OFF_O);
+    float *qs = reinterpret_cast<float *>(smem + Cfg::OFF_Q);
+    float *ps = reinterpret_cast<float *>(smem + Cfg::OFF_P) + warp * 16 * GM;
+    float2 *mls = reinterpret_cast<float2 *>(smem + Cfg::OFF_ML);
+    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MASK) + warp * Cfg::ST;
+    const uint32_t ring = sm100::smem_addr(smem) + tid * 16;
+
+    PagedWalk w;
+    long long at, chunk;
+    const int tiles = paged_range(p, w, at, chunk);
+    if (tid == 0) paged_record(p, w, tiles, chunk);
+    if (!tiles) return;
+    __syncthreads();
+
+    PagedWalk lw = w;
+    int issued = 0, page = paged_entry(p, lw, warp, lane);
+    auto issue = [&]() {
+        if (issued < tiles) {
+            const int stage = issued % Cfg::ST, h = lw.u / p.nsub;
+            const int row = paged_entry_row(p, lw, warp, lane, page);
+            const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);
+            if (lane == 0) masks[stage] = mask;
+            if (mask) {
+                const size_t bh = (size_t)lw.b * c.Hkv + h;
+                const uint32_t dst = ring + stage * Cfg::STAGE;
+                const T *kn = (const T *)p.k + bh * c.dqk, *vn = (const T *)p.v + bh * c.dv;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rw = __shfl_sync(0xffffffffu, row, i * 8 + r);
+                    const T *src = rw == kPagedNew ? kn : (const T *)c.kp + (size_t)max(rw, 0) * c.dqk;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        if (j * 16 < c.dqk)
+                            paged_load4(dst + (i * (D / 16) + j) * (16 * kPagedThreads), src, j * 16 + cq * 4, c.dqk,
+                                        rw != kPagedNone, p.vec);
+                }
+#pragma unroll
+                for (int i = 0; i < Cfg::VP; ++i) {
+                    const int rw = __shfl_sync(0xffffffffu, row, i * Cfg::TP + vrow);
+                    const T *src = rw == kPagedNew ? vn : (const T *)c.vp + (size_t)max(rw, 0) * c.dv;
+                    paged_load4(dst + (Cfg::KP + i) * (16 * kPagedThreads), src, vcol, c.dv, rw != kPagedNone, p.vec);
+                }
+            }
+            if (++issued < tiles) {
+                lw.next(p);
+                page = paged_entry(p, lw, warp, lane);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < Cfg::ST - 1; ++s) issue();
+
+    float4 o[GM];
+    float m[GM], l[GM];
+    int t0 = 0;
+    for (int it = 0; it < tiles; ++it) {
+        const int h = w.u / p.nsub, sub = w.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
+        const size_t hq0 = (size_t)w.b * p.Hq + h * p.g + sub * p.gs;
+        if (it == 0 || w.tile == 0) {
+            t0 = w.tile;
+            __syncthreads();   // the queries of the last unit are read
+            for (int i = tid; i < GM * D; i += kPagedThreads) {
+                const int row = i / D, col = i - row * D;
+                qs[i] = row < rows && col < c.dqk ? ld((const T *)p.q + (hq0 + row) * c.dqk + col) * p.scale_log2 : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < GM; ++n) {
+                o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+                m[n] = -INFINITY;
+                l[n] = 0.f;
+            }
+        }
+        cp_async_wait<Cfg::ST - 2>();
+        __syncwarp();
+        const int stage = it % Cfg::ST;
+        const uint32_t mask = masks[stage];
+        issue();
+        if (mask) {
+            const uint32_t src = ring + stage * Cfg::STAGE;
+            float s[2][GM];
+#pragma unroll
+            for (int n = 0; n < GM; ++n) s[0][n] = s[1][n] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                if (j * 16 >= c.dqk) break;
+                const float4 k0 = lds_f4(src + j * (16 * kPagedThreads));
+                const float4 k1 = lds_f4(src + (D / 16 + j) * (16 * kPagedThreads));
+#pragma unroll
+                for (int n = 0; n < GM; ++n) {
+                    if (n >= rows) break;
+                    const float4 x = *reinterpret_cast<const float4 *>(qs + n * D + j * 16 + cq * 4);
+                    s[0][n] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[0][n]))));
+                    s[1][n] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[1][n]))));
+                }
+            }
+            float al[GM];
+#pragma unroll
+            for (int n = 0; n < GM; ++n) {
+                if (n >= rows) break;
+                float mx = m[n];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = s[i][n];
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    s[i][n] = x = mask >> (i * 8 + r) & 1 ? x : -INFINITY;
+                    mx = fmaxf(mx, x);
+                    if (p.scores && cq == 0)
+                        p.scores[(hq0 + n) * p.stride + w.tile * kPagedTile + warp * 16 + i * 8 + r] = x;
+                }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                const float base = mx == -INFINITY ? 0.f : mx;
+                al[n] = exp2f(m[n] - base);
+                m[n] = mx;
+                const float e0 = exp2f(s[0][n] - base), e1 = exp2f(s[1][n] - base);
+                l[n] = l[n] * al[n] + e0 + e1;
+                if (cq == (n & 3)) {
+                    ps[r * GM + n] = e0;
+                    ps[(8 + r) * GM + n] = e1;
+                }
+                o[n].x *= al[n];
+                o[n].y *= al[n];
+                o[n].z *= al[n];
+                o[n].w *= al[n];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < Cfg::VP; ++i) {
+                const float4 x = lds_f4(src + (Cfg::KP + i) * (16 * kPagedThreads));
+                const float *pp = ps + (i * Cfg::TP + vrow) * GM;
+#pragma unroll
+                for (int n = 0; n < GM; ++n) {
+                    if (n >= rows) break;
+                    const float f = pp[n];
+                    o[n].x = fmaf(f, x.x, o[n].x);
+                    o[n].y = fmaf(f, x.y, o[n].y);
+                    o[n].z = fmaf(f, x.z, o[n].z);
+                    o[n].w = fmaf(f, x.w, o[n].w);
+                }
+            }
+        } else if (p.scores && w.n > 0 && cq == 0) {
+            for (int n = 0; n < rows; ++n)
+                for (int i = 0; i < 2; ++i)
+                    p.scores[(hq0 + n) * p.stride + w.tile * kPagedTile + warp * 16 + i * 8 + r] = -INFINITY;
+        }
+        __syncwarp();   // the weights are read before the next tile's
+        if (w.tile == w.nt - 1 || it == tiles - 1) {
+            bool whole;
+            const int slot = paged_part(p, w, t0, at + it, whole);
+            if (w.n < 0) {
+                if (w.u == 0 && tid == 0) report(kStatusCheck);
+            } else {
+#pragma unroll
+                for (int n = 0; n < GM; ++n) {   // a slot's weight is held by its quad's four lanes alike
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], off);
+                    if (Cfg::TP == 2) {
+                        o[n].x += __shfl_xor_sync(0xffffffffu, o[n].x, 16);
+                        o[n].y += __shfl_xor_sync(0xffffffffu, o[n].y, 16);
+                        o[n].z += __shfl_xor_sync(0xffffffffu, o[n].z, 16);
+                        o[n].w += __shfl_xor_sync(0xffffffffu, o[n].w, 16);
+                    }
+                    if (lane == 0) mls[warp * kPagedRows + n] = make_float2(m[n], l[n]);
+                }
+#pragma unroll
+                for (int n0 = 0; n0 < GM; n0 += 8) {
+#pragma unroll
+                    for (int n = n0; n < GM && n < n0 + 8; ++n)
+                        if (vrow == 0) *reinterpret_cast<float4 *>(obuf + (warp * 8 + n - n0) * D + vcol) = o[n];
+                    __syncthreads();
+                    paged_merge<T, D>(p, w, obuf, mls, n0, min(rows, GM), whole, slot);
+                    __syncthreads();
+                }
+                if (p.k && sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
+            }
+        }
+        if (it < tiles - 1) w.next(p);
+    }
+    cp_async_wait<0>();
+}
+
+// Maximum and sum of row `row` over the parts of a unit that crosses ranges.
+__device__ __forceinline__ float2 paged_part_ml(const PagedDecodeParams &p, int g0, int i, int row)
+{
+    return p.ml[((size_t)(g0 + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows + row];
+}
+
+// Joins a unit's parts.  The K ranges that hold them share the work: their
+// blocks take equal slices of the unit's rows x dv outputs, and within a warp
+// a power of two of lanes shares one output's parts.
+template <typename T>
+__device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const PagedSpan &s, long long chunk)
+{
+    const int g0 = (int)(s.first / chunk), g1 = (int)((s.end - 1) / chunk), K = g1 - g0 + 1, dv = p.c.dv;
+    const int h = s.u / p.nsub, sub = s.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
+    const size_t hq0 = (size_t)s.b * p.Hq + h * p.g + sub * p.gs;
+    const int E = rows * dv, idx = blockIdx.x - g0;
+    const int e0 = (int)((long long)E * idx / K), e1 = (int)((long long)E * (idx + 1) / K);
+    int KL = 1;
+    while (KL < K && KL < 32) KL <<= 1;
+    const int sub_lane = threadIdx.x % KL;
+    for (int base = e0; base < e1; base += kPagedThreads / KL) {   // the same count for every thread
+        const int e = base + threadIdx.x / KL;
+        const bool on = e < e1;
+        const int row = on ? e / dv : 0, col = on ? e - row * dv : 0;
+        float M = -INFINITY;
+        for (int i = sub_lane; i < K; i += KL) M = fmaxf(M, paged_part_ml(p, g0, i, row).x);
+        for (int off = 1; off < KL; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float b = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc = 0.f;
+        for (int i = sub_lane; i < K; i += KL) {
+            const float2 e2 = paged_part_ml(p, g0, i, row);
+            const float f = exp2f(e2.x - b);
+            L = fmaf(f, e2.y, L);
+            acc = fmaf(f, p.part[(((size_t)(g0 + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows + row) * dv + col], acc);
+        }
+        for (int off = 1; off < KL; off <<= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, off);
+            acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        }
+        if (on && sub_lane == 0) {
+            const bool none = L == 0.f;
+            st((T *)p.y + (hq0 + row) * dv + col, none ? 0.f : acc / L);
+            if (col == 0 && p.lse) p.lse[hq0 + row] = none ? -INFINITY : M * 0.693147180559945309f + logf(L);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedDecodeParams p)
 {
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
-    __shared__ float qs[128], sc[kPagedThreads], red[kPagedThreads / 32];
-    __shared__ int rows[kPagedThreads];
+    __shared__ float lse2[kPagedMaxGroup];
+    const PagedRecord rec = p.rec[blockIdx.x];
+    if (!rec.tiles) return;
+    if (rec.head.b >= 0) paged_join<T>(p, rec.head, rec.chunk);
+    if (rec.tail.b >= 0) paged_join<T>(p, rec.tail, rec.chunk);
+    if (!p.w_out) return;
+    // weights of the range's slots, each head's first unit for all its units
     const PagedCache &c = p.c;
     const int tid = threadIdx.x;
-    const size_t bh = blockIdx.x;
-    const int b = (int)(bh / c.Hkv), h = (int)(bh - (size_t)b * c.Hkv), g = p.Hq / c.Hkv;
-    const int len = c.lens[b], pos = p.pos ? p.pos[b] : 0;
-    if (len < 0 || len > c.cap() - (p.k ? 1 : 0) || pos < 0) {
-        if (tid == 0) report(kStatusCheck);
-        return;
-    }
-    const int n = len + (p.k ? 1 : 0);
-    T *kp = (T *)c.kp, *vp = (T *)c.vp;
-    if (p.k) {
-        const int row = paged_row(c, b, h, len);
-        if (row >= 0) {
-            if (tid < c.dqk) kp[(size_t)row * c.dqk + tid] = ((const T *)p.k)[bh * c.dqk + tid];
-            if (tid < c.dv) vp[(size_t)row * c.dv + tid] = ((const T *)p.v)[bh * c.dv + tid];
-        }
-        if (p.positions && tid == 0 && row >= 0) p.positions[bh * c.cap() + len] = pos;
-        __syncthreads();
-    }
-    for (int j = 0; j < g; ++j) {
-        const size_t hq = (size_t)b * p.Hq + h * g + j;
-        __syncthreads();
-        if (tid < c.dqk) qs[tid] = ld((const T *)p.q + hq * c.dqk + tid);
-        __syncthreads();
-        auto score = [&](int t, int &row) {
-            row = t < n ? paged_row(c, b, h, t) : -1;
-            if (t < n && row < 0) report(kStatusCheck);
-            if (row < 0) return -INFINITY;
-            float s = 0.f;
-            for (int i = 0; i < c.dqk; ++i) s = fmaf(qs[i], ld(kp + (size_t)row * c.dqk + i), s);
-            return s * p.scale;
-        };
-        float m = -INFINITY, z = 0.f, acc = 0.f;
-        for (int t0 = 0; t0 < n; t0 += kPagedThreads) {
-            int row;
-            const float s = score(t0 + tid, row);
-            const float mn = fmaxf(m, block_reduce<kPagedThreads>(s, true, red));
-            const float base = mn == -INFINITY ? 0.f : mn;   // nothing but -inf so far: exp(-inf) = 0
-            const float e = expf(s - base), a = expf(m - base);
-            sc[tid] = e;
-            rows[tid] = row;
-            z = z * a + block_reduce<kPagedThreads>(row < 0 ? 0.f : e, false, red);
-            m = mn;
-            acc *= a;
-            if (tid < c.dv)
-                for (int i = 0; i < min(kPagedThreads, n - t0); ++i)
-                    if (rows[i] >= 0) acc = fmaf(sc[i], ld(vp + (size_t)rows[i] * c.dv + tid), acc);
-        }
-        if (tid < c.dv) st((T *)p.y + hq * c.dv + tid, n ? acc / z : 0.f);
-        const float lse = n ? m + logf(z) : -INFINITY;
-        if (p.lse && tid == 0) p.lse[hq] = lse;
-        if (p.w_out)
-            for (int t = tid; t < n; t += kPagedThreads) {
-                int row;
-                const float s = score(t, row);
-                const size_t at = bh * c.cap() + t;
-                const float old = j ? p.w_out[at] : t == len ? 0.f : p.w_in[at];
-                p.w_out[at] = old + (row < 0 ? 0.f : expf(s - lse));
+    PagedWalk w;
+    w.b = rec.b;
+    w.u = rec.u;
+    w.tile = rec.tile;
+    w.load(p);
+    long long at = blockIdx.x * rec.chunk;
+    for (int left = rec.tiles; left > 0;) {
+        const int here = min(left, w.nt - w.tile);
+        if (w.u % p.nsub == 0 && w.n > 0) {
+            const int h = w.u / p.nsub;
+            const size_t hq0 = (size_t)w.b * p.Hq + h * p.g, bh = (size_t)w.b * c.Hkv + h;
+            __syncthreads();
+            for (int j = tid; j < p.g; j += kPagedThreads) {
+                const int sub = j / p.gs;
+                const long long first = at - w.tile + (long long)sub * w.nt;   // of this head's unit
+                const int g0 = (int)(first / rec.chunk), g1 = (int)((first + w.nt - 1) / rec.chunk);
+                if (g0 == g1) {
+                    lse2[j] = p.lse2[hq0 + j];
+                } else {
+                    float M = -INFINITY, L = 0.f;
+                    for (int i = 0; i <= g1 - g0; ++i) M = fmaxf(M, paged_part_ml(p, g0, i, j - sub * p.gs).x);
+                    for (int i = 0; i <= g1 - g0; ++i) {
+                        const float2 e = paged_part_ml(p, g0, i, j - sub * p.gs);
+                        L = fmaf(exp2f(e.x - (M == -INFINITY ? 0.f : M)), e.y, L);
+                    }
+                    lse2[j] = L == 0.f ? -INFINITY : M + log2f(L);
+                }
             }
+            __syncthreads();
+            const int end = min(w.n, (w.tile + here) * kPagedTile);
+            for (int t = w.tile * kPagedTile + tid; t < end; t += kPagedThreads) {
+                float sum = 0.f;
+                for (int j = 0; j < p.g; ++j)
+                    if (lse2[j] != -INFINITY) sum += exp2f(p.scores[(hq0 + j) * p.stride + t] - lse2[j]);
+                const size_t to = bh * c.cap() + t;
+                p.w_out[to] = (p.k && t == w.n - 1 ? 0.f : p.w_in[to]) + sum;
+            }
+        }
+        left -= here;
+        at += here;
+        if (left > 0) {
+            w.tile += here - 1;
+            w.next(p);
+        }
     }
 }
 
@@ -229,30 +1029,6 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     if (!(w == w)) w = -INFINITY;
     const uint32_t u = __float_as_uint(w + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// Exclusive prefix of x over the block in thread order, and the total.
-template <int NT>
-__device__ __forceinline__ int block_scan(int x, int *part, int &total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = x;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += o;
-    }
-    __syncthreads();
-    if (lane == 31) part[warp] = s;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        if (i < warp) before += part[i];
-        total += part[i];
-    }
-    return before + s - x;
 }
 
 // One block per (b, h): a radix select over the weights' keys (four passes of
@@ -333,13 +1109,13 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_select_kernel(const
         const bool in = t < n, r = in && recent(t);
         const uint32_t key = in && r == cls ? weight_key(w[t]) : 0;
         const bool eq = in && r == cls && key == thr;
-        const int rank = ties + block_scan<kEvictThreads>(eq, part, total);
+        const int rank = ties + block_scan<kEvictThreads>((int)eq, part, total);
         ties += total;
         const bool keep = in && (r == cls ? key > thr || (eq && rank < need) : r);
         const bool hole = in && t < budget && !keep, mover = keep && t >= budget;
-        const int ih = nh + block_scan<kEvictThreads>(hole, part, total);
+        const int ih = nh + block_scan<kEvictThreads>((int)hole, part, total);
         nh += total;
-        const int im = nm + block_scan<kEvictThreads>(mover, part, total);
+        const int im = nm + block_scan<kEvictThreads>((int)mover, part, total);
         nm += total;
         if (hole) holes[ih] = t;
         if (mover) movers[im] = t;

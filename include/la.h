@@ -393,9 +393,11 @@ LA_API size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, i
  *   positions nullable, with pos (both or neither) and only with k, v:
  *      positions[b,h,lens[b]] = pos[b].
  *   workspace at least la_paged_decode_workspace_bytes(...) bytes.
- * n = 0 gives y = 0 and lse = -inf.  Slots past n are not read: what stale
- * pages hold does not matter.
- * Errors: LA_ERR_INVALID_ARG also when Hq is not a multiple of Hkv. */
+ * Where nothing is attended to (n = 0, only pages out of range, or every score
+ * -inf) y = 0 and lse = -inf.  Slots past n are not read: what stale pages
+ * hold does not matter.
+ * Errors: LA_ERR_INVALID_ARG also when Hq is not a multiple of Hkv;
+ * LA_ERR_UNSUPPORTED for more than 128 query heads per key/value head. */
 LA_API la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse,
                                       void *k_pages, void *v_pages, const int32_t *block_table, const int32_t *lens,
                                       const float *weights_in, float *weights_out, int32_t *positions,

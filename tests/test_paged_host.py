@@ -71,10 +71,11 @@ def test_step_arguments_refused(lib):
                dict(wi=0x10000, wo=0x10010),                         # overlapping, not the same
                dict(wi=0x10002, wo=0x20000)):
         assert _step(lib, **kw) == 1, kw
+    assert _step(lib, Hq=258) == 2                 # 129 query heads on one key/value head
     need = la.la_paged_decode_workspace_bytes(2, 4, 2, 64, 64, 16, 4, True, la.LA_BF16)
-    if need:
-        w = dict(wi=0x10000, wo=0x10000)
-        assert _step(lib, wsb=need - 1, **w) == 1 and _step(lib, ws=None, **w) == 1 and _step(lib, ws=0x100004, **w) == 1
+    w = dict(wi=0x10000, wo=0x10000)
+    assert _step(lib, wsb=need - 1, **w) == 1 and _step(lib, ws=None, **w) == 1 and _step(lib, ws=0x100004, **w) == 1
+    assert la.la_paged_decode_workspace_bytes(2, 4, 2, 64, 64, 16, 4, False, la.LA_BF16) < need
 
 
 def test_evict_arguments_refused(lib):
