@@ -711,7 +711,9 @@ static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_si
     pl->mma = dtype == LA_BF16 && dqk % 8 == 0 && dv % 8 == 0;
     pl->nsub = (g + kPagedRows - 1) / kPagedRows;
     pl->gs = (g + pl->nsub - 1) / pl->nsub;
-    pl->grid = kNumSms * (pl->mma || (dqk <= 64 && dv <= 64) ? 2 : 1);
+    // as many blocks as an SM holds (BLOCKS of the kernels' configurations)
+    const bool narrow = dqk <= 64 && dv <= 64;
+    pl->grid = kNumSms * (pl->mma ? (narrow ? 3 : 2) : (narrow ? 2 : 1));
     const int64_t tiles = ((int64_t)max_pages * page_size + kPagedTile - 1) / kPagedTile;
     pl->stride = tiles * kPagedTile;
     // a range's length and a unit's tiles are 32-bit
@@ -720,12 +722,34 @@ static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_si
     return LA_OK;
 }
 
+// The pool as rows of d elements, boxes of `rows` x 128 bytes in SW128.
+static bool make_pool_map(CUtensorMap *m, const void *base, const PagedCache &c, int d, int rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)c.num_pages * c.Hkv * c.page};
+    cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DQ, int DV, bool HI>
-static la_status paged_mma_run(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+static la_status paged_mma_run(PagedDecodeParams p, const PagedPlan &pl, cudaStream_t st)
 {
     using Cfg = PagedMma<DQ, DV, HI>;
+    // a chunk of 16 slots starts at a multiple of 16, so a box of `rows` slots,
+    // rows a power of two that divides the page size, never leaves its page
+    p.box_rows = 16;
+    while (p.c.page % p.box_rows) p.box_rows /= 2;
+    const int rows = p.box_rows < 4 ? 1 : p.box_rows;
+    CUtensorMap tk, tv;
+    if (!make_pool_map(&tk, p.c.kp, p.c, p.c.dqk, rows) || !make_pool_map(&tv, p.c.vp, p.c, p.c.dv, rows))
+        return LA_ERR_CUDA;
     if (set_smem<paged_decode_mma_kernel<DQ, DV, HI>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
-    return launch_pdl(paged_decode_mma_kernel<DQ, DV, HI>, pl.grid, kPagedThreads, Cfg::SMEM, st, p);
+    return launch_pdl(paged_decode_mma_kernel<DQ, DV, HI>, pl.grid, kPagedThreads, Cfg::SMEM, st, tk, tv, p);
 }
 
 static la_status paged_mma(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)

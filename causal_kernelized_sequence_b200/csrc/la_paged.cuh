@@ -144,6 +144,7 @@ struct PagedDecodeParams {
     int Hq, g, nsub, gs;     // query heads; per key/value head; units per head; heads per unit
     float scale_log2;        // log2(e) / sqrt(dqk)
     bool vec;                // rows start on 16-byte boundaries
+    int box_rows;            // slots per TMA box: 16, 8 or 4, or below 4: gathered by fours
     PagedRecord *rec;        // [grid]
     float2 *ml;              // [grid][2][16]: running maximum and sum of the head and tail parts
     float *part;             // [grid][2][16][dv]: their accumulators
@@ -205,10 +206,12 @@ struct PagedWalk {
     }
 };
 
-// This block's range: sets the walk to its start and returns its number of tiles.
-__device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk &w, long long &first, long long &chunk)
+// This block's range: sets the walk to its start and returns its number of
+// tiles.  `part`: kPagedWarps + 2 words of shared memory.
+__device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk &w, long long &first, long long &chunk,
+                                           long long *part)
 {
-    __shared__ long long part[kPagedWarps], found[2];
+    long long *found = part + kPagedWarps;
     const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
     const int slab = (B + kPagedThreads - 1) / kPagedThreads, b0 = min(B, tid * slab), b1 = min(B, b0 + slab);
     long long mine = 0, total;
@@ -389,107 +392,141 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
 
 // bf16, dqk and dv multiples of 8, on the tensor cores with mma.sync: the work
 // per byte (2 * heads FLOP) is far below what a tcgen05 tile is for, and its 16
-// rows hold the query heads.  Operands go from global memory to the registers
-// of the thread that needs them, through 16-byte slots of shared memory that
-// only this thread writes and reads (cp.async, `ST` tiles deep), so nothing but
-// the wait for its own copies orders a warp.  No transpose is needed, because
-// a sum does not depend on the order of its terms and a matrix product not on
-// the order of its columns:
-//   S = Q K^T  thread (r = lane / 4, c = lane % 4) holds 8 consecutive
-//       coordinates 32 j + 8 c .. + 7 of key r (and r + 8): the two k-steps
-//       2j, 2j + 1 take them as their coordinates 2c, 2c+1, 2c+8, 2c+9; Q is
-//       held in the same order.
-//   O = P V    thread (r, c) holds the values 64 j + 8 r .. + 7 of the slots
-//       2c, 2c+1, 2c+8, 2c+9: a byte permutation pairs two slots, and column
-//       block e of the product is the values 64 j + 8 r + e.
+// rows hold the query heads.  Each warp brings the 16 slots of its next tiles
+// into its own ring of shared memory by TMA, `ST` deep, with one mbarrier per
+// stage: slots of a page are neighbouring rows of the pool, so a box of
+// `box_rows` rows (16, 8 or 4, whichever divides the page size) and 64 columns
+// is one copy; pages of other sizes gather four rows by index.  Nothing but the
+// wait for its own copies orders a warp inside a unit.
+//
+// The operands go from shared memory to the MMA's registers without a
+// transpose, because a sum does not depend on the order of its terms and a
+// matrix product not on the order of its columns:
+//   S = Q K^T  thread (r = lane / 4, c = lane % 4) reads 8 consecutive
+//       coordinates 32 j + 8 c .. + 7 of key slot(r) (and 8 + slot(r)): the two
+//       k-steps 2j, 2j + 1 take them as their coordinates 2c, 2c+1, 2c+8,
+//       2c+9; Q is held in the same order.
+//   O = P V    thread (r, c) reads the values 64 j + 8 r .. + 7 of the slots
+//       slot(2c), slot(2c+1) and 8 more: a byte permutation pairs two slots, and
+//       column block e of the product is the values 64 j + 8 r + e.
+// The permutation slot() of 0..7 lets both reads touch every bank once: a copy
+// stores 16-byte piece i of row t at piece i ^ (t mod 8), eight lanes read at a
+// time, and they are rows slot(2i), slot(2i+1) (which differ in bit 2) for K and
+// rows slot(0), slot(2), slot(4), slot(6) (which differ above bit 0) for V.
+//
 // P enters as two bf16 halves, p = hi + lo (error 2^-17 of p instead of 2^-9).
 // With at most 8 heads (HI false) the low half takes the rows 8..15, which are
 // free, and costs no further MMA.
 template <int DQ, int DV, bool HI>
 struct PagedMma {
-    static constexpr int KP = DQ / 16, VP = DV / 16;           // 16-byte pieces per thread and tile
-    static constexpr int STAGE = (KP + VP) * 16 * kPagedThreads;
+    static constexpr int KB = DQ / 64, VB = DV / 64;           // 64-column blocks
+    static constexpr int BLOCK = 16 * 128;                     // 16 slots x 128 bytes
+    static constexpr int STAGE = (KB + VB) * BLOCK;            // per warp
     static constexpr int ST = DQ + DV > 128 ? 3 : 4;
-    static constexpr int OFF_O = ST * STAGE;
+    static constexpr int OFF_O = kPagedWarps * ST * STAGE;
     static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * DV * 4;
-    static constexpr int OFF_MASK = OFF_ML + kPagedWarps * kPagedRows * 8;
+    static constexpr int OFF_BAR = OFF_ML + kPagedWarps * kPagedRows * 8;
+    static constexpr int OFF_MASK = OFF_BAR + kPagedWarps * ST * 8;
     static constexpr int SMEM = OFF_MASK + kPagedWarps * ST * 4;
-    static constexpr int BLOCKS = 2;                           // per SM
+    static constexpr int BLOCKS = DQ + DV > 128 ? 2 : 3;       // per SM
 };
+
+__device__ __forceinline__ int paged_slot(int r)
+{
+    return ((r ^ r >> 2) & 1) << 2 | (r & 2) | r >> 2;
+}
 
 template <int DQ, int DV, bool HI>
 __global__ void __launch_bounds__(kPagedThreads, PagedMma<DQ, DV, HI>::BLOCKS)
-paged_decode_mma_kernel(const PagedDecodeParams p)
+paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const PagedDecodeParams p)
 {
     using Cfg = PagedMma<DQ, DV, HI>;
     using T = __nv_bfloat16;
-    extern __shared__ __align__(128) uint8_t smem[];
-    sm100::grid_dependency_wait();
-    sm100::launch_dependents();
+    using namespace sm100;
+    extern __shared__ __align__(1024) uint8_t smem[];   // SW128 tiles from the start; no static shared memory before it
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
     float *obuf = reinterpret_cast<float *>(smem + Cfg::OFF_O);
     float2 *mls = reinterpret_cast<float2 *>(smem + Cfg::OFF_ML);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR) + warp * Cfg::ST;
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MASK) + warp * Cfg::ST;
-    const uint32_t ring = sm100::smem_addr(smem) + tid * 16;
+    uint8_t *ring = smem + warp * Cfg::ST * Cfg::STAGE;
+    if (lane == 0) {
+        for (int i = 0; i < Cfg::ST; ++i) mbar_init(full + i, 1);
+        mbar_init_fence();
+        if (warp == 0) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+        }
+    }
+    grid_dependency_wait();
+    launch_dependents();
 
     PagedWalk w;
     long long at, chunk;
-    const int tiles = paged_range(p, w, at, chunk);
+    const int tiles = paged_range(p, w, at, chunk, reinterpret_cast<long long *>(obuf));
     if (tid == 0) paged_record(p, w, tiles, chunk);
     if (!tiles) return;
-    __syncthreads();   // the record is written before paged_part adds to it
+    __syncthreads();   // the barriers are set, and the record is written before paged_part adds to it
 
-    // loads: `lw` is the tile whose loads are next, `page` its table entries
+    // loads: `lw` is the tile whose loads are next, `page` its table entries.
+    // Slots past the end and on bad pages are not brought in: what their rows
+    // of a stage hold is masked.
     PagedWalk lw = w;
-    int issued = 0, page = paged_entry(p, lw, warp, lane);
+    int issued = 0, stage_in = 0, page = paged_entry(p, lw, warp, lane);
+    bool alive = true;          // false once a wait ran out: no more loads, no more work
+    uint32_t pending = 0, phases = 0;
+    constexpr uint32_t kCopied = 1u << 16;   // beside a stage's mask: there are copies to wait for
     auto issue = [&]() {
-        if (issued < tiles) {
-            const int stage = issued % Cfg::ST, h = lw.u / p.nsub;
-            const int row = paged_entry_row(p, lw, warp, lane, page);
-            const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);
-            if (lane == 0) masks[stage] = mask;
-            if (mask) {
-                const size_t bh = (size_t)lw.b * c.Hkv + h;
-                const uint32_t dst = ring + stage * Cfg::STAGE;
-                const T *kn = (const T *)p.k + bh * c.dqk, *vn = (const T *)p.v + bh * c.dv;
+        if (issued >= tiles || !alive) return;
+        const int row = paged_entry_row(p, lw, warp, lane, page);
+        const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);   // slots attended to
+        const uint32_t held = __ballot_sync(0xffffffffu, row >= 0);             // of them, in the pool
+        const int group = p.box_rows < 4 ? 4 : p.box_rows;                      // slots per copy
+        // a box lies in one page: its first slot is held if any is; four gathered
+        // rows are brought in if any is held (row 0 in place of the others)
+        const bool mine = lane < 16 && (lane & (group - 1)) == 0 && (held >> lane & ((1u << group) - 1));
+        const uint32_t copies = __ballot_sync(0xffffffffu, mine);
+        int y[4];
+        if (p.box_rows < 4) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rw = __shfl_sync(0xffffffffu, row, i * 8 + r);
-                    const T *src = rw == kPagedNew ? kn : (const T *)c.kp + (size_t)max(rw, 0) * c.dqk;
+            for (int i = 0; i < 4; ++i) y[i] = max(__shfl_sync(0xffffffffu, row, (lane + i) & 15), 0);
+        }
+        if (lane == 0) {
+            masks[stage_in] = mask | (copies ? kCopied : 0u);
+            if (copies) mbar_arrive_expect_tx(full + stage_in, __popc(copies) * group * 128 * (Cfg::KB + Cfg::VB));
+        }
+        __syncwarp();
+        if (mine) {
+            uint8_t *dst = ring + stage_in * Cfg::STAGE + lane * 128;
 #pragma unroll
-                    for (int j = 0; j < DQ / 32; ++j) {
-                        const int col = j * 32 + cq * 8;
-                        const bool ok = rw != kPagedNone && col < c.dqk;
-                        cp_async16(dst + (i * (DQ / 32) + j) * (16 * kPagedThreads), ok ? src + col : src, ok);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rw = __shfl_sync(0xffffffffu, row, 2 * cq + (i & 1) + (i >> 1) * 8);
-                    const T *src = rw == kPagedNew ? vn : (const T *)c.vp + (size_t)max(rw, 0) * c.dv;
-#pragma unroll
-                    for (int j = 0; j < DV / 64; ++j) {
-                        const int col = j * 64 + r * 8;
-                        const bool ok = rw != kPagedNone && col < c.dv;
-                        cp_async16(dst + (Cfg::KP + j * 4 + i) * (16 * kPagedThreads), ok ? src + col : src, ok);
-                    }
-                }
-            }
-            if (++issued < tiles) {
-                lw.next(p);
-                page = paged_entry(p, lw, warp, lane);
+            for (int j = 0; j < Cfg::KB + Cfg::VB; ++j) {
+                const CUtensorMap *map = j < Cfg::KB ? &tm_k : &tm_v;
+                const int x = (j < Cfg::KB ? j : j - Cfg::KB) * 64;
+                if (p.box_rows < 4) tma_gather4(dst + j * Cfg::BLOCK, map, full + stage_in, x, y[0], y[1], y[2], y[3]);
+                else tma_load_2d(dst + j * Cfg::BLOCK, map, full + stage_in, x, row);
             }
         }
-        cp_async_commit();
+        if (copies) pending |= 1u << stage_in;
+        if (++stage_in == Cfg::ST) stage_in = 0;
+        if (++issued < tiles) {
+            lw.next(p);
+            page = paged_entry(p, lw, warp, lane);
+        }
     };
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < Cfg::ST - 1; ++s) issue();
+
+    const int sk = paged_slot(r), sv0 = paged_slot(2 * cq), sv1 = paged_slot(2 * cq + 1);
+    const uint32_t off_k = sk * 128 + ((cq ^ sk) << 4);   // coordinates 32 j + ..: ^ 64 for odd j, + a block per two
+    const uint32_t off_v0 = Cfg::KB * Cfg::BLOCK + sv0 * 128 + ((r ^ sv0) << 4);
+    const uint32_t off_v1 = Cfg::KB * Cfg::BLOCK + sv1 * 128 + ((r ^ sv1) << 4);
 
     constexpr int NR = HI ? 2 : 1;   // rows of a thread: r and r + 8
     uint4 qf[DQ / 32][NR];
     float o[DV / 8][4], m[NR], l[NR];
-    int t0 = 0;
+    int t0 = 0, stage = 0;
     for (int it = 0; it < tiles; ++it) {
         const int h = w.u / p.nsub, sub = w.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
         const size_t hq0 = (size_t)w.b * p.Hq + h * p.g + sub * p.gs;
@@ -512,26 +549,54 @@ paged_decode_mma_kernel(const PagedDecodeParams p)
                 l[i] = 0.f;
             }
         }
-        cp_async_wait<Cfg::ST - 2>();
         __syncwarp();
-        const int stage = it % Cfg::ST;
-        const uint32_t mask = masks[stage];
+        uint32_t mask = masks[stage];
+        if ((mask & kCopied) && alive) {
+            alive = mbar_wait(full + stage, phases >> stage & 1);
+            alive = __all_sync(0xffffffffu, alive);
+            phases ^= 1u << stage;
+            if (alive) pending &= ~(1u << stage);
+        }
         issue();   // into the stage of the tile before, which every lane has used
+        mask = alive ? mask & 0xffffu : 0u;
+        uint8_t *src_g = ring + stage * Cfg::STAGE;
+        if (++stage == Cfg::ST) stage = 0;
         if (mask) {
-            const uint32_t src = ring + stage * Cfg::STAGE;
+            const uint32_t src = smem_addr(src_g);
+            const int last = w.n - 1 - (w.tile * kPagedTile + warp * 16);   // the new token's slot in this chunk
+            if (p.k && last >= 0 && last < 16 && (mask >> last & 1)) {
+                // its row of the stage is stale: the caller's k, v take its place (zeros past dqk, dv, as in a copy)
+                const size_t bh = (size_t)w.b * c.Hkv + h;
+#pragma unroll
+                for (int j = 0; j < (DQ + DV + 255) / 256; ++j) {
+                    const int i = lane + 32 * j;   // 16-byte piece of (k, v)
+                    const bool isk = i < DQ / 8;
+                    const int x = isk ? i : i - DQ / 8;
+                    if (i < (DQ + DV) / 8) {
+                        const bool in = x * 8 < (isk ? c.dqk : c.dv);
+                        const T *from = isk ? (const T *)p.k + bh * c.dqk : (const T *)p.v + bh * c.dv;
+                        uint8_t *to = src_g + (isk ? 0 : Cfg::KB * Cfg::BLOCK) + (x >> 3) * Cfg::BLOCK + last * 128 +
+                                      (((x & 7) ^ (last & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(to) =
+                            in ? *reinterpret_cast<const uint4 *>(from + x * 8) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async();   // before a later copy writes this stage
+                __syncwarp();
+            }
             float s[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
                 for (int j = 0; j < DQ / 32; ++j) {
-                    const uint4 kk = lds128(src + (i * (DQ / 32) + j) * (16 * kPagedThreads));
+                    const uint4 kk = lds128(src + (j >> 1) * Cfg::BLOCK + i * 1024 + (off_k ^ (j & 1) * 64));
                     const uint4 a = qf[j][0], b = HI ? qf[j][NR - 1] : make_uint4(0u, 0u, 0u, 0u);
                     mma_16816(s[i], a.x, b.x, a.y, b.y, kk.x, kk.y);
                     mma_16816(s[i], a.z, b.z, a.w, b.w, kk.z, kk.w);
                 }
             }
-            // scores in log2 units; slot of s[i][e] (and s[i][e + 2]): 8 i + 2 cq + e
+            // scores in log2 units; slot of s[i][e] (and s[i][e + 2]): 8 i + sv_e
             float mn[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -541,15 +606,19 @@ paged_decode_mma_kernel(const PagedDecodeParams p)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float &x = s[i][n * 2 + e];
-                        x = mask >> (8 * i + 2 * cq + e) & 1 ? x * p.scale_log2 : -INFINITY;
+                        x *= p.scale_log2;
+                        if (mask != 0xffffu && !(mask >> (8 * i + (e ? sv1 : sv0)) & 1)) x = -INFINITY;
                         mn[n] = fmaxf(mn[n], x);
                     }
                 mn[n] = fmaxf(mn[n], __shfl_xor_sync(0xffffffffu, mn[n], 1));
                 mn[n] = fmaxf(mn[n], __shfl_xor_sync(0xffffffffu, mn[n], 2));
                 if (p.scores && r + 8 * n < rows) {
-                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16 + 2 * cq;
-                    *reinterpret_cast<float2 *>(to) = make_float2(s[0][n * 2], s[0][n * 2 + 1]);
-                    *reinterpret_cast<float2 *>(to + 8) = make_float2(s[1][n * 2], s[1][n * 2 + 1]);
+                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        to[8 * i + sv0] = s[i][n * 2];
+                        to[8 * i + sv1] = s[i][n * 2 + 1];
+                    }
                 }
             }
             bool grew = mn[0] != m[0];
@@ -570,7 +639,7 @@ paged_decode_mma_kernel(const PagedDecodeParams p)
                     o[i][3] *= al[NR - 1];
                 }
             }
-            uint32_t hi[2][NR], lo[2][NR];   // [slots 2cq.. / 2cq + 8..][row]
+            uint32_t hi[2][NR], lo[2][NR];   // [slots sv. / 8 + sv.][row]
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float base = m[n] == -INFINITY ? 0.f : m[n];
@@ -587,7 +656,12 @@ paged_decode_mma_kernel(const PagedDecodeParams p)
                 if (j * 64 >= c.dv) break;
                 uint4 vv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) vv[i] = lds128(src + (Cfg::KP + j * 4 + i) * (16 * kPagedThreads));
+                for (int i = 0; i < 4; ++i) {
+                    vv[i] = lds128(src + (i & 1 ? off_v1 : off_v0) + (i >> 1) * 1024 + j * Cfg::BLOCK);
+                    // a masked slot's weight is 0, but its row may hold anything: 0 * NaN is NaN
+                    if (mask != 0xffffu && !(mask >> ((i >> 1) * 8 + (i & 1 ? sv1 : sv0)) & 1))
+                        vv[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
@@ -605,9 +679,9 @@ paged_decode_mma_kernel(const PagedDecodeParams p)
 #pragma unroll
             for (int n = 0; n < NR; ++n)
                 if (r + 8 * n < rows) {
-                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16 + 2 * cq;
-                    *reinterpret_cast<float2 *>(to) = make_float2(-INFINITY, -INFINITY);
-                    *reinterpret_cast<float2 *>(to + 8) = make_float2(-INFINITY, -INFINITY);
+                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) to[8 * i + sv0] = to[8 * i + sv1] = -INFINITY;
                 }
         }
         if (w.tile == w.nt - 1 || it == tiles - 1) {   // the unit, or its part in this range, ends
@@ -648,7 +722,10 @@ paged_decode_mma_kernel(const PagedDecodeParams p)
         }
         if (it < tiles - 1) w.next(p);
     }
-    cp_async_wait<0>();
+    // after a wait that ran out, let this warp's own copies land before leaving (bounded)
+    if (!alive)
+        for (int i = 0; i < Cfg::ST; ++i)
+            if (pending >> i & 1) mbar_wait(full + i, phases >> i & 1, 100000000ull);
 }
 
 // fp32, and bf16 rows that do not start on 16-byte boundaries: the same walk
@@ -706,7 +783,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSimt<T, D, GM>::BLOCKS)
 paged_decode_simt_kernel(const PagedDecodeParams p)
 {
     using Cfg = PagedSimt<T, D, GM>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
     const PagedCache &c = p.c;
@@ -721,7 +798,7 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
 
     PagedWalk w;
     long long at, chunk;
-    const int tiles = paged_range(p, w, at, chunk);
+    const int tiles = paged_range(p, w, at, chunk, reinterpret_cast<long long *>(obuf));
     if (tid == 0) paged_record(p, w, tiles, chunk);
     if (!tiles) return;
     __syncthreads();
