@@ -698,7 +698,7 @@ static la_status check_paged_ptrs(const void *kp, const void *vp, const int32_t 
 // tiles per block.
 struct PagedPlan {
     bool mma;
-    int nsub, gs, grid;
+    int nsub, gs, grid, tile;
     int64_t stride;   // slots per row of kept scores: whole tiles
     size_t ml_off() const { return ((size_t)grid * sizeof(PagedRecord) + 15) / 16 * 16; }
 };
@@ -714,8 +714,9 @@ static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_si
     // as many blocks as an SM holds (BLOCKS of the kernels' configurations)
     const bool narrow = dqk <= 64 && dv <= 64;
     pl->grid = kNumSms * (pl->mma ? (narrow ? 3 : 2) : (narrow ? 2 : 1));
-    const int64_t tiles = ((int64_t)max_pages * page_size + kPagedTile - 1) / kPagedTile;
-    pl->stride = tiles * kPagedTile;
+    pl->tile = pl->mma ? 7 : 6;
+    const int64_t tiles = (((int64_t)max_pages * page_size - 1) >> pl->tile) + 1;
+    pl->stride = tiles << pl->tile;
     // a range's length and a unit's tiles are 32-bit
     if ((int64_t)B * Hkv * pl->nsub >= (int64_t)1 << 31 || (double)tiles * B * Hkv * pl->nsub / pl->grid >= 2e9)
         return LA_ERR_INVALID_ARG;
@@ -740,9 +741,9 @@ template <int DQ, int DV, bool HI>
 static la_status paged_mma_run(PagedDecodeParams p, const PagedPlan &pl, cudaStream_t st)
 {
     using Cfg = PagedMma<DQ, DV, HI>;
-    // a chunk of 16 slots starts at a multiple of 16, so a box of `rows` slots,
-    // rows a power of two that divides the page size, never leaves its page
-    p.box_rows = 16;
+    // a chunk of 32 slots starts at a multiple of 32, so a box of a power of two
+    // of slots that divides the page size never leaves its page
+    p.box_rows = 32;
     while (p.c.page % p.box_rows) p.box_rows /= 2;
     const int rows = p.box_rows < 4 ? 1 : p.box_rows;
     CUtensorMap tk, tv;
@@ -1323,6 +1324,7 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
     p.g = Hq / Hkv;
     p.nsub = pl.nsub;
     p.gs = pl.gs;
+    p.tile = pl.tile;
     p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)dqk));
     p.vec = rows16(dqk, dtype) && rows16(dv, dtype);
     uint8_t *ws = (uint8_t *)workspace;

@@ -3,6 +3,9 @@
 // eviction by accumulated attention weight.
 #pragma once
 
+#include <limits.h>
+#include <type_traits>
+
 #include "la_device.cuh"
 #include "sm100.cuh"
 
@@ -104,8 +107,8 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 // unit's slots are cut into tiles of 64.  All tiles of the call, in (b, h, tile)
 // order, are dealt out in equal contiguous ranges, one per block: one long
 // sequence or many ragged ones load every SM alike, and each block finds its
-// range from lens by one scan.  Inside a tile each of the four warps owns 16
-// slots, with its own running maximum, sum and accumulators, so warps meet only
+// range from lens by one scan.  Inside a tile each of the four warps owns a quarter
+// of the slots, with its own running maximum, sum and accumulators, so warps meet only
 // where a unit ends.  A unit inside one range is finished there; the parts of
 // one that crosses ranges go to the workspace and the join kernel adds them,
 // in the order of the ranges:  with M = max m_i,
@@ -115,7 +118,6 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 
 constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
-constexpr int kPagedTile = 64;
 constexpr int kPagedRows = 16;       // query heads of a unit
 constexpr int kPagedMaxGroup = 128;  // query heads per key/value head
 
@@ -142,9 +144,10 @@ struct PagedDecodeParams {
     int *positions;
     const int *pos;
     int Hq, g, nsub, gs;     // query heads; per key/value head; units per head; heads per unit
+    int tile;                // log2 of the slots per tile
     float scale_log2;        // log2(e) / sqrt(dqk)
     bool vec;                // rows start on 16-byte boundaries
-    int box_rows;            // slots per TMA box: 16, 8 or 4, or below 4: gathered by fours
+    int box_rows;            // slots per TMA box: 32, 16, 8 or 4, or below 4: gathered by fours
     PagedRecord *rec;        // [grid]
     float2 *ml;              // [grid][2][16]: running maximum and sum of the head and tail parts
     float *part;             // [grid][2][16][dv]: their accumulators
@@ -160,7 +163,10 @@ __device__ __forceinline__ int paged_count(const PagedDecodeParams &p, int b)
     if (len < 0 || len > p.c.cap() - more || (p.pos && p.pos[b] < 0)) return -1;
     return len + more;
 }
-__device__ __forceinline__ int paged_tiles(int n) { return n <= 0 ? 1 : (n + kPagedTile - 1) / kPagedTile; }
+__device__ __forceinline__ int paged_tiles(const PagedDecodeParams &p, int n)
+{
+    return n <= 0 ? 1 : ((n - 1) >> p.tile) + 1;
+}
 
 // Exclusive prefix of x over the block in thread order, and the total.
 template <int NT, typename I>
@@ -186,24 +192,33 @@ __device__ __forceinline__ I block_scan(I x, I *part, I &total)
     return before + s - x;
 }
 
-// A position in the (b, unit, tile) order.
+// A position in the (b, h, sub, tile) order; (h, sub) is a unit, u = h nsub + sub.
 struct PagedWalk {
-    int b, u, tile, nt, n;
+    int b, h, sub, tile, nt, n;
     __device__ __forceinline__ void load(const PagedDecodeParams &p)
     {
         n = paged_count(p, b);
-        nt = paged_tiles(n);
+        nt = paged_tiles(p, n);
     }
     // to the next tile (not past the last sequence)
     __device__ __forceinline__ void next(const PagedDecodeParams &p)
     {
         if (++tile < nt) return;
         tile = 0;
-        if (++u < p.c.Hkv * p.nsub) return;
-        u = 0;
+        if (++sub < p.nsub) return;
+        sub = 0;
+        if (++h < p.c.Hkv) return;
+        h = 0;
         ++b;
         load(p);
     }
+    __device__ __forceinline__ int rows(const PagedDecodeParams &p) const { return min(p.gs, p.g - sub * p.gs); }
+    // its first query head, and its key/value head, of all sequences
+    __device__ __forceinline__ size_t hq(const PagedDecodeParams &p) const
+    {
+        return (size_t)b * p.Hq + h * p.g + sub * p.gs;
+    }
+    __device__ __forceinline__ size_t bh(const PagedDecodeParams &p) const { return (size_t)b * p.c.Hkv + h; }
 };
 
 // This block's range: sets the walk to its start and returns its number of
@@ -215,7 +230,7 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
     const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
     const int slab = (B + kPagedThreads - 1) / kPagedThreads, b0 = min(B, tid * slab), b1 = min(B, b0 + slab);
     long long mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += paged_tiles(paged_count(p, b));
+    for (int b = b0; b < b1; ++b) mine += paged_tiles(p, paged_count(p, b));
     long long before = block_scan<kPagedThreads>(mine, part, total);
     total *= U;
     chunk = (total + gridDim.x - 1) / gridDim.x;
@@ -224,7 +239,7 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
     if (first < total && x >= before && x < before + mine) {
         int b = b0;
         for (;; ++b) {
-            const int nt = paged_tiles(paged_count(p, b));
+            const int nt = paged_tiles(p, paged_count(p, b));
             if (x < before + nt) break;
             before += nt;
         }
@@ -236,8 +251,10 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
     w.b = (int)found[0];
     w.load(p);
     const long long off = first - U * found[1];   // below U * nt
-    w.u = (int)(off / w.nt);
-    w.tile = (int)(off - (long long)w.u * w.nt);
+    const int u = (int)(off / w.nt);
+    w.h = u / p.nsub;
+    w.sub = u - w.h * p.nsub;
+    w.tile = (int)(off - (long long)u * w.nt);
     return (int)(total - first < chunk ? total - first : chunk);
 }
 
@@ -250,7 +267,7 @@ __device__ __forceinline__ void paged_record(const PagedDecodeParams &p, const P
     r.tiles = tiles;
     r.chunk = chunk;
     r.b = w.b;
-    r.u = w.u;
+    r.u = w.h * p.nsub + w.sub;
     r.tile = w.tile;
 }
 
@@ -262,7 +279,7 @@ __device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const Pa
                                             const float2 *mls, int r0, int rows, bool whole, int slot)
 {
     const int tid = threadIdx.x, col = tid % DV;
-    const size_t hq0 = (size_t)w.b * p.Hq + (w.u / p.nsub) * p.g + (w.u % p.nsub) * p.gs;
+    const size_t hq0 = w.hq(p);
     for (int r = tid / DV; r < 8 && r0 + r < rows; r += kPagedThreads / DV) {
         float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll
@@ -295,8 +312,8 @@ template <typename T>
 __device__ __forceinline__ void paged_store_new(const PagedDecodeParams &p, const PagedWalk &w)
 {
     const PagedCache &c = p.c;
-    const int h = w.u / p.nsub, t = w.n - 1, row = paged_row(c, w.b, h, t), tid = threadIdx.x;
-    const size_t bh = (size_t)w.b * c.Hkv + h;
+    const int t = w.n - 1, row = paged_row(c, w.b, w.h, t), tid = threadIdx.x;
+    const size_t bh = w.bh(p);
     if (row < 0) return;
     for (int i = tid; i < c.dqk; i += kPagedThreads) ((T *)c.kp)[(size_t)row * c.dqk + i] = ((const T *)p.k)[bh * c.dqk + i];
     for (int i = tid; i < c.dv; i += kPagedThreads) ((T *)c.vp)[(size_t)row * c.dv + i] = ((const T *)p.v)[bh * c.dv + i];
@@ -316,34 +333,40 @@ __device__ __forceinline__ int paged_part(const PagedDecodeParams &p, const Page
         s.first = at - w.tile;
         s.end = s.first + w.nt;
         s.b = w.b;
-        s.u = w.u;
+        s.u = w.h * p.nsub + w.sub;
     }
     return slot;
 }
 
 constexpr int kPagedNone = -1, kPagedNew = -2;   // rows that are not in the pool
 
-// Row of slot t0 + lane (lanes 0..15) of the walk's unit: kPagedNone past the
-// end or on a bad page, kPagedNew for the new token, which is read from the
-// caller's k, v.  `page` is the table's entry, fetched earlier.
-__device__ __forceinline__ int paged_entry(const PagedDecodeParams &p, const PagedWalk &w, int warp, int lane)
+// Row of slot t of the walk's unit: kPagedNone past the end or on a bad page,
+// kPagedNew for the new token, which is read from the caller's k, v.  `page` is
+// the table's entry, fetched earlier by paged_entry.
+__device__ __forceinline__ int paged_entry(const PagedDecodeParams &p, const PagedWalk &w, int t)
 {
-    const int t = w.tile * kPagedTile + warp * 16 + lane;
-    if (lane >= 16 || t >= w.n) return -1;
+    if (t >= w.n) return -1;
     return p.c.table[(size_t)w.b * p.c.max_pages + (p.c.shift >= 0 ? t >> p.c.shift : t / p.c.page)];
 }
-__device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const PagedWalk &w, int warp, int lane, int page)
+__device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const PagedWalk &w, int t, int page)
 {
     const PagedCache &c = p.c;
-    const int t = w.tile * kPagedTile + warp * 16 + lane;
-    if (lane >= 16 || t >= w.n) return kPagedNone;
+    if (t >= w.n) return kPagedNone;
     if ((unsigned)page >= (unsigned)c.num_pages) {
         report(kStatusCheck);
         return kPagedNone;
     }
     if (p.k && t == w.n - 1) return kPagedNew;
     const int off = c.shift >= 0 ? t & (c.page - 1) : t % c.page;
-    return (page * c.Hkv + w.u / p.nsub) * c.page + off;
+    return (page * c.Hkv + w.h) * c.page + off;
+}
+
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // 16 bytes from global to shared memory, or 16 zero bytes.
@@ -392,22 +415,22 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
 
 // bf16, dqk and dv multiples of 8, on the tensor cores with mma.sync: the work
 // per byte (2 * heads FLOP) is far below what a tcgen05 tile is for, and its 16
-// rows hold the query heads.  Each warp brings the 16 slots of its next tiles
-// into its own ring of shared memory by TMA, `ST` deep, with one mbarrier per
-// stage: slots of a page are neighbouring rows of the pool, so a box of
-// `box_rows` rows (16, 8 or 4, whichever divides the page size) and 64 columns
-// is one copy; pages of other sizes gather four rows by index.  Nothing but the
-// wait for its own copies orders a warp inside a unit.
+// rows hold the query heads.  Each warp brings the keys, then the values, of its
+// next 32 slots into its own ring of shared memory by TMA, `ST` loads deep, with
+// one mbarrier per place: slots of a page are neighbouring rows of the pool, so a
+// box of `box_rows` rows (32, 16, 8 or 4, whichever divides the page size) and 64
+// columns is one copy; pages of other sizes gather four rows by index.  Nothing
+// but the wait for its own copies orders a warp inside a unit.
 //
 // The operands go from shared memory to the MMA's registers without a
 // transpose, because a sum does not depend on the order of its terms and a
 // matrix product not on the order of its columns:
 //   S = Q K^T  thread (r = lane / 4, c = lane % 4) reads 8 consecutive
-//       coordinates 32 j + 8 c .. + 7 of key slot(r) (and 8 + slot(r)): the two
-//       k-steps 2j, 2j + 1 take them as their coordinates 2c, 2c+1, 2c+8,
-//       2c+9; Q is held in the same order.
+//       coordinates 32 j + 8 c .. + 7 of key slot(r) (+ 8 i): the two k-steps
+//       2j, 2j + 1 take them as their coordinates 2c, 2c+1, 2c+8, 2c+9; Q is
+//       held in the same order.
 //   O = P V    thread (r, c) reads the values 64 j + 8 r .. + 7 of the slots
-//       slot(2c), slot(2c+1) and 8 more: a byte permutation pairs two slots, and
+//       slot(2c), slot(2c+1) (+ 8 i): a byte permutation pairs two slots, and
 //       column block e of the product is the values 64 j + 8 r + e.
 // The permutation slot() of 0..7 lets both reads touch every bank once: a copy
 // stores 16-byte piece i of row t at piece i ^ (t mod 8), eight lanes read at a
@@ -420,15 +443,15 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
 template <int DQ, int DV, bool HI>
 struct PagedMma {
     static constexpr int KB = DQ / 64, VB = DV / 64;           // 64-column blocks
-    static constexpr int BLOCK = 16 * 128;                     // 16 slots x 128 bytes
-    static constexpr int STAGE = (KB + VB) * BLOCK;            // per warp
-    static constexpr int ST = DQ + DV > 128 ? 3 : 4;
-    static constexpr int OFF_O = kPagedWarps * ST * STAGE;
+    static constexpr int BLOCK = 32 * 128;                     // 32 slots x 128 bytes
+    static constexpr int PLACE = (KB > VB ? KB : VB) * BLOCK;  // one load: a warp's keys or values
+    static constexpr int ST = PLACE > BLOCK ? 3 : 4;
+    static constexpr int OFF_O = kPagedWarps * ST * PLACE;
     static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * DV * 4;
     static constexpr int OFF_BAR = OFF_ML + kPagedWarps * kPagedRows * 8;
-    static constexpr int OFF_MASK = OFF_BAR + kPagedWarps * ST * 8;
-    static constexpr int SMEM = OFF_MASK + kPagedWarps * ST * 4;
-    static constexpr int BLOCKS = DQ + DV > 128 ? 2 : 3;       // per SM
+    static constexpr int OFF_MASK = OFF_BAR + kPagedWarps * ST * 8;      // [warp][4] (slots attended to, copies made)
+    static constexpr int SMEM = OFF_MASK + kPagedWarps * 4 * 8;
+    static constexpr int BLOCKS = PLACE > BLOCK ? 2 : 3;       // per SM
 };
 
 __device__ __forceinline__ int paged_slot(int r)
@@ -444,14 +467,15 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     using Cfg = PagedMma<DQ, DV, HI>;
     using T = __nv_bfloat16;
     using namespace sm100;
+    constexpr uint32_t ALL = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t smem[];   // SW128 tiles from the start; no static shared memory before it
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
     float *obuf = reinterpret_cast<float *>(smem + Cfg::OFF_O);
     float2 *mls = reinterpret_cast<float2 *>(smem + Cfg::OFF_ML);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR) + warp * Cfg::ST;
-    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MASK) + warp * Cfg::ST;
-    uint8_t *ring = smem + warp * Cfg::ST * Cfg::STAGE;
+    uint2 *masks = reinterpret_cast<uint2 *>(smem + Cfg::OFF_MASK) + warp * 4;
+    uint8_t *ring = smem + warp * Cfg::ST * Cfg::PLACE;
     if (lane == 0) {
         for (int i = 0; i < Cfg::ST; ++i) mbar_init(full + i, 1);
         mbar_init_fence();
@@ -470,76 +494,108 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     if (!tiles) return;
     __syncthreads();   // the barriers are set, and the record is written before paged_part adds to it
 
-    // loads: `lw` is the tile whose loads are next, `page` its table entries.
-    // Slots past the end and on bad pages are not brought in: what their rows
-    // of a stage hold is masked.
+    // Loads, keys and values of a tile in turn.  `lw` is the tile whose loads are
+    // next and `page` its table entries, one slot per lane.  Slots past the end
+    // and on bad pages are not brought in: what their rows hold is masked.
     PagedWalk lw = w;
-    int issued = 0, stage_in = 0, page = paged_entry(p, lw, warp, lane);
+    auto slot_in = [&]() { return (lw.tile << 7) + warp * 32 + lane; };
+    int issued = 0, place_in = 0, page = paged_entry(p, lw, slot_in()), row = 0;
+    uint32_t copies = 0, pending = 0, phases = 0;
     bool alive = true;          // false once a wait ran out: no more loads, no more work
-    uint32_t pending = 0, phases = 0;
-    constexpr uint32_t kCopied = 1u << 16;   // beside a stage's mask: there are copies to wait for
+    const int group = p.box_rows < 4 ? 4 : p.box_rows;         // slots per copy
+    const uint32_t group_mask = group == 32 ? ALL : (1u << group) - 1;
     auto issue = [&]() {
-        if (issued >= tiles || !alive) return;
-        const int row = paged_entry_row(p, lw, warp, lane, page);
-        const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);   // slots attended to
-        const uint32_t held = __ballot_sync(0xffffffffu, row >= 0);             // of them, in the pool
-        const int group = p.box_rows < 4 ? 4 : p.box_rows;                      // slots per copy
-        // a box lies in one page: its first slot is held if any is; four gathered
-        // rows are brought in if any is held (row 0 in place of the others)
-        const bool mine = lane < 16 && (lane & (group - 1)) == 0 && (held >> lane & ((1u << group) - 1));
-        const uint32_t copies = __ballot_sync(0xffffffffu, mine);
-        int y[4];
-        if (p.box_rows < 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = max(__shfl_sync(0xffffffffu, row, (lane + i) & 15), 0);
-        }
-        if (lane == 0) {
-            masks[stage_in] = mask | (copies ? kCopied : 0u);
-            if (copies) mbar_arrive_expect_tx(full + stage_in, __popc(copies) * group * 128 * (Cfg::KB + Cfg::VB));
-        }
-        __syncwarp();
-        if (mine) {
-            uint8_t *dst = ring + stage_in * Cfg::STAGE + lane * 128;
-#pragma unroll
-            for (int j = 0; j < Cfg::KB + Cfg::VB; ++j) {
-                const CUtensorMap *map = j < Cfg::KB ? &tm_k : &tm_v;
-                const int x = (j < Cfg::KB ? j : j - Cfg::KB) * 64;
-                if (p.box_rows < 4) tma_gather4(dst + j * Cfg::BLOCK, map, full + stage_in, x, y[0], y[1], y[2], y[3]);
-                else tma_load_2d(dst + j * Cfg::BLOCK, map, full + stage_in, x, row);
+        if (issued >= 2 * tiles || !alive) return;
+        const bool isv = issued & 1;
+        if (!isv) {
+            row = paged_entry_row(p, lw, slot_in(), page);
+            const uint32_t mask = __ballot_sync(ALL, row != kPagedNone);   // slots attended to
+            const uint32_t held = __ballot_sync(ALL, row >= 0);            // of them, in the pool
+            // a box lies in one page: its first slot is held if any is; four gathered
+            // rows are brought in if any is held (row 0 in place of the others)
+            copies = __ballot_sync(ALL, (lane & (group - 1)) == 0 && (held >> lane & group_mask));
+            if (lane == 0) masks[issued >> 1 & 3] = make_uint2(mask, copies);
+            if ((issued >> 1) + 1 < tiles) {
+                lw.next(p);
+                page = paged_entry(p, lw, slot_in());
             }
         }
-        if (copies) pending |= 1u << stage_in;
-        if (++stage_in == Cfg::ST) stage_in = 0;
-        if (++issued < tiles) {
-            lw.next(p);
-            page = paged_entry(p, lw, warp, lane);
+        if (copies) {
+            const CUtensorMap *map = isv ? &tm_v : &tm_k;
+            if (lane == 0)
+                mbar_arrive_expect_tx(full + place_in, __popc(copies) * group * 128 * (isv ? Cfg::VB : Cfg::KB));
+            int y1, y2, y3;
+            if (p.box_rows < 4) {
+                y1 = max(__shfl_down_sync(ALL, row, 1), 0);
+                y2 = max(__shfl_down_sync(ALL, row, 2), 0);
+                y3 = max(__shfl_down_sync(ALL, row, 3), 0);
+            }
+            __syncwarp();
+            if (copies >> lane & 1) {
+                uint8_t *dst = ring + place_in * Cfg::PLACE + lane * 128;
+#pragma unroll
+                for (int j = 0; j < (Cfg::KB > Cfg::VB ? Cfg::KB : Cfg::VB); ++j) {
+                    if (j >= (isv ? Cfg::VB : Cfg::KB)) break;
+                    if (p.box_rows < 4)
+                        tma_gather4(dst + j * Cfg::BLOCK, map, full + place_in, j * 64, max(row, 0), y1, y2, y3);
+                    else
+                        tma_load_2d(dst + j * Cfg::BLOCK, map, full + place_in, j * 64, row);
+                }
+            }
+            pending |= 1u << place_in;
         }
+        ++issued;
+        if (++place_in == Cfg::ST) place_in = 0;
+    };
+    // the next place of the ring, once its copies have landed
+    int place = 0;
+    auto take = [&](bool copied) {
+        if (copied && alive) {
+            alive = __all_sync(ALL, mbar_wait(full + place, phases >> place & 1));
+            if (alive) {
+                phases ^= 1u << place;
+                pending &= ~(1u << place);
+            }
+        }
+        uint8_t *at_place = ring + place * Cfg::PLACE;
+        if (++place == Cfg::ST) place = 0;
+        return at_place;
+    };
+    // The new token's row of a place is stale: the caller's k or v takes its
+    // place (zeros past d, as in a copy).
+    auto patch = [&](uint8_t *dst, const T *src, int d, int blocks, int slot) {
+        if (lane < blocks * 8) {
+            const uint4 x = lane * 8 < d ? *reinterpret_cast<const uint4 *>(src + lane * 8) : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(dst + (lane >> 3) * Cfg::BLOCK + slot * 128 + (((lane ^ slot) & 7) << 4)) = x;
+        }
+        fence_proxy_async();   // before a later copy writes this place
+        __syncwarp();
     };
 #pragma unroll 1
     for (int s = 0; s < Cfg::ST - 1; ++s) issue();
 
     const int sk = paged_slot(r), sv0 = paged_slot(2 * cq), sv1 = paged_slot(2 * cq + 1);
     const uint32_t off_k = sk * 128 + ((cq ^ sk) << 4);   // coordinates 32 j + ..: ^ 64 for odd j, + a block per two
-    const uint32_t off_v0 = Cfg::KB * Cfg::BLOCK + sv0 * 128 + ((r ^ sv0) << 4);
-    const uint32_t off_v1 = Cfg::KB * Cfg::BLOCK + sv1 * 128 + ((r ^ sv1) << 4);
+    const uint32_t off_v0 = sv0 * 128 + ((r ^ sv0) << 4), off_v1 = sv1 * 128 + ((r ^ sv1) << 4);
 
     constexpr int NR = HI ? 2 : 1;   // rows of a thread: r and r + 8
     uint4 qf[DQ / 32][NR];
     float o[DV / 8][4], m[NR], l[NR];
-    int t0 = 0, stage = 0;
+    int t0 = 0, rows = 0;
+    size_t hq0 = 0;
     for (int it = 0; it < tiles; ++it) {
-        const int h = w.u / p.nsub, sub = w.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
-        const size_t hq0 = (size_t)w.b * p.Hq + h * p.g + sub * p.gs;
         if (it == 0 || w.tile == 0) {   // a new unit
             t0 = w.tile;
+            rows = w.rows(p);
+            hq0 = w.hq(p);
 #pragma unroll
             for (int j = 0; j < DQ / 32; ++j)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    const int col = j * 32 + cq * 8, row = r + 8 * i;
+                    const int col = j * 32 + cq * 8, row_q = r + 8 * i;
                     qf[j][i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < rows && col < c.dqk)
-                        qf[j][i] = *reinterpret_cast<const uint4 *>((const T *)p.q + (hq0 + row) * c.dqk + col);
+                    if (row_q < rows && col < c.dqk)
+                        qf[j][i] = *reinterpret_cast<const uint4 *>((const T *)p.q + (hq0 + row_q) * c.dqk + col);
                 }
 #pragma unroll
             for (int i = 0; i < DV / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -550,84 +606,66 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
             }
         }
         __syncwarp();
-        uint32_t mask = masks[stage];
-        if ((mask & kCopied) && alive) {
-            alive = mbar_wait(full + stage, phases >> stage & 1);
-            alive = __all_sync(0xffffffffu, alive);
-            phases ^= 1u << stage;
-            if (alive) pending &= ~(1u << stage);
-        }
-        issue();   // into the stage of the tile before, which every lane has used
-        mask = alive ? mask & 0xffffu : 0u;
-        uint8_t *src_g = ring + stage * Cfg::STAGE;
-        if (++stage == Cfg::ST) stage = 0;
-        if (mask) {
-            const uint32_t src = smem_addr(src_g);
-            const int last = w.n - 1 - (w.tile * kPagedTile + warp * 16);   // the new token's slot in this chunk
-            if (p.k && last >= 0 && last < 16 && (mask >> last & 1)) {
-                // its row of the stage is stale: the caller's k, v take its place (zeros past dqk, dv, as in a copy)
-                const size_t bh = (size_t)w.b * c.Hkv + h;
+        const uint2 mk = masks[it & 3];
+        const bool copied = mk.y != 0;
+        const uint32_t mask = mk.x;
+        float *const sc = p.scores ? p.scores + (hq0 + r) * p.stride + (w.tile << 7) + warp * 32 : nullptr;
+        const int last = p.k ? w.n - 1 - ((w.tile << 7) + warp * 32) : -1;   // the new token's slot in this chunk
+        const bool fresh = last >= 0 && last < 32 && (mask >> last & 1);
+
+        // one tile; `whole`: every slot is attended to
+        auto work = [&](auto whole_tag) {
+            constexpr bool WHOLE = decltype(whole_tag)::value;
+            uint8_t *kp = take(copied);
+            issue();   // into the place before, which every lane has used
+            if (!alive) return;
+            if (fresh) patch(kp, (const T *)p.k + w.bh(p) * c.dqk, c.dqk, Cfg::KB, last);
+            const uint32_t ks = smem_addr(kp);
+            float s[4][4];
 #pragma unroll
-                for (int j = 0; j < (DQ + DV + 255) / 256; ++j) {
-                    const int i = lane + 32 * j;   // 16-byte piece of (k, v)
-                    const bool isk = i < DQ / 8;
-                    const int x = isk ? i : i - DQ / 8;
-                    if (i < (DQ + DV) / 8) {
-                        const bool in = x * 8 < (isk ? c.dqk : c.dv);
-                        const T *from = isk ? (const T *)p.k + bh * c.dqk : (const T *)p.v + bh * c.dv;
-                        uint8_t *to = src_g + (isk ? 0 : Cfg::KB * Cfg::BLOCK) + (x >> 3) * Cfg::BLOCK + last * 128 +
-                                      (((x & 7) ^ (last & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(to) =
-                            in ? *reinterpret_cast<const uint4 *>(from + x * 8) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-                fence_proxy_async();   // before a later copy writes this stage
-                __syncwarp();
-            }
-            float s[2][4];
+            for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            for (int j = 0; j < DQ / 32; ++j) {
+                const uint4 a = qf[j][0], b = HI ? qf[j][NR - 1] : make_uint4(0u, 0u, 0u, 0u);
+                uint4 kk[4];
 #pragma unroll
-                for (int j = 0; j < DQ / 32; ++j) {
-                    const uint4 kk = lds128(src + (j >> 1) * Cfg::BLOCK + i * 1024 + (off_k ^ (j & 1) * 64));
-                    const uint4 a = qf[j][0], b = HI ? qf[j][NR - 1] : make_uint4(0u, 0u, 0u, 0u);
-                    mma_16816(s[i], a.x, b.x, a.y, b.y, kk.x, kk.y);
-                    mma_16816(s[i], a.z, b.z, a.w, b.w, kk.z, kk.w);
-                }
+                for (int i = 0; i < 4; ++i) kk[i] = lds128(ks + (j >> 1) * Cfg::BLOCK + i * 1024 + (off_k ^ (j & 1) * 64));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_16816(s[i], a.x, b.x, a.y, b.y, kk[i].x, kk[i].y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_16816(s[i], a.z, b.z, a.w, b.w, kk[i].z, kk[i].w);
             }
             // scores in log2 units; slot of s[i][e] (and s[i][e + 2]): 8 i + sv_e
             float mn[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                mn[n] = m[n];
+                mn[n] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float &x = s[i][n * 2 + e];
                         x *= p.scale_log2;
-                        if (mask != 0xffffu && !(mask >> (8 * i + (e ? sv1 : sv0)) & 1)) x = -INFINITY;
+                        if (!WHOLE && !(mask >> (8 * i + (e ? sv1 : sv0)) & 1)) x = -INFINITY;
                         mn[n] = fmaxf(mn[n], x);
                     }
-                mn[n] = fmaxf(mn[n], __shfl_xor_sync(0xffffffffu, mn[n], 1));
-                mn[n] = fmaxf(mn[n], __shfl_xor_sync(0xffffffffu, mn[n], 2));
-                if (p.scores && r + 8 * n < rows) {
-                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16;
+                mn[n] = fmaxf(mn[n], __shfl_xor_sync(ALL, mn[n], 1));
+                mn[n] = fmaxf(mn[n], __shfl_xor_sync(ALL, mn[n], 2));
+                mn[n] = fmaxf(mn[n], m[n]);
+                if (sc && r + 8 * n < rows)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        to[8 * i + sv0] = s[i][n * 2];
-                        to[8 * i + sv1] = s[i][n * 2 + 1];
+                    for (int i = 0; i < 4; ++i) {
+                        sc[8 * n * p.stride + 8 * i + sv0] = s[i][n * 2];
+                        sc[8 * n * p.stride + 8 * i + sv1] = s[i][n * 2 + 1];
                     }
-                }
             }
             bool grew = mn[0] != m[0];
             if (HI) grew |= mn[NR - 1] != m[NR - 1];
-            if (__any_sync(0xffffffffu, grew)) {
+            if (__any_sync(ALL, grew)) {
                 float al[NR];
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
-                    al[n] = exp2f(m[n] - (mn[n] == -INFINITY ? 0.f : mn[n]));
+                    al[n] = ex2(m[n] - (mn[n] == -INFINITY ? 0.f : mn[n]));
                     l[n] *= al[n];
                     m[n] = mn[n];
                 }
@@ -639,61 +677,81 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                     o[i][3] *= al[NR - 1];
                 }
             }
-            uint32_t hi[2][NR], lo[2][NR];   // [slots sv. / 8 + sv.][row]
+            uint32_t hi[4][NR], lo[4][NR];   // [slots 8 i + sv.][row]
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float base = m[n] == -INFINITY ? 0.f : m[n];
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float e0 = exp2f(s[i][n * 2] - base), e1 = exp2f(s[i][n * 2 + 1] - base);
-                    l[n] += e0 + e1;
+                for (int i = 0; i < 4; ++i) {
+                    const float e0 = ex2(s[i][n * 2] - base), e1 = ex2(s[i][n * 2 + 1] - base);
+                    sum += e0 + e1;
                     hi[i][n] = bf16x2(e0, e1);
                     lo[i][n] = bf16x2_rest(e0, e1, hi[i][n]);
                 }
+                l[n] += sum;
             }
+            uint8_t *vp = take(copied);
+            issue();
+            if (!alive) return;
+            if (fresh) patch(vp, (const T *)p.v + w.bh(p) * c.dv, c.dv, Cfg::VB, last);
+            const uint32_t vs = smem_addr(vp);
 #pragma unroll
             for (int j = 0; j < DV / 64; ++j) {
                 if (j * 64 >= c.dv) break;
-                uint4 vv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    vv[i] = lds128(src + (i & 1 ? off_v1 : off_v0) + (i >> 1) * 1024 + j * Cfg::BLOCK);
-                    // a masked slot's weight is 0, but its row may hold anything: 0 * NaN is NaN
-                    if (mask != 0xffffu && !(mask >> ((i >> 1) * 8 + (i & 1 ? sv1 : sv0)) & 1))
-                        vv[i] = make_uint4(0u, 0u, 0u, 0u);
-                }
+                for (int kk = 0; kk < 2; ++kk) {
+                    uint4 vv[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t b0 = __byte_perm(word(vv[0], e / 2), word(vv[1], e / 2), sel);
-                    const uint32_t b1 = __byte_perm(word(vv[2], e / 2), word(vv[3], e / 2), sel);
-                    if (HI) {
-                        mma_16816(o[j * 8 + e], hi[0][0], hi[0][NR - 1], hi[1][0], hi[1][NR - 1], b0, b1);
-                        mma_16816(o[j * 8 + e], lo[0][0], lo[0][NR - 1], lo[1][0], lo[1][NR - 1], b0, b1);
-                    } else {
-                        mma_16816(o[j * 8 + e], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b0, b1);
+                    for (int i = 0; i < 4; ++i) {
+                        vv[i] = lds128(vs + (i & 1 ? off_v1 : off_v0) + (2 * kk + (i >> 1)) * 1024 + j * Cfg::BLOCK);
+                        // a masked slot's weight is 0, but its row may hold anything: 0 * NaN is NaN
+                        if (!WHOLE && !(mask >> ((2 * kk + (i >> 1)) * 8 + (i & 1 ? sv1 : sv0)) & 1))
+                            vv[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t b0 = __byte_perm(word(vv[0], e / 2), word(vv[1], e / 2), sel);
+                        const uint32_t b1 = __byte_perm(word(vv[2], e / 2), word(vv[3], e / 2), sel);
+                        float(&d)[4] = o[j * 8 + e];
+                        if (HI) {
+                            mma_16816(d, hi[2 * kk][0], hi[2 * kk][NR - 1], hi[2 * kk + 1][0], hi[2 * kk + 1][NR - 1], b0, b1);
+                            mma_16816(d, lo[2 * kk][0], lo[2 * kk][NR - 1], lo[2 * kk + 1][0], lo[2 * kk + 1][NR - 1], b0, b1);
+                        } else {
+                            mma_16816(d, hi[2 * kk][0], lo[2 * kk][0], hi[2 * kk + 1][0], lo[2 * kk + 1][0], b0, b1);
+                        }
                     }
                 }
             }
-        } else if (p.scores && w.n > 0) {   // slots past the end, or on bad pages: no weight
+        };
+        if (mask == ALL) {
+            work(std::true_type{});
+        } else if (mask) {
+            work(std::false_type{});
+        } else {   // slots past the end, or on bad pages: no weight
+            if (sc && w.n > 0)
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-                if (r + 8 * n < rows) {
-                    float *to = p.scores + (hq0 + r + 8 * n) * p.stride + w.tile * kPagedTile + warp * 16;
+                for (int n = 0; n < NR; ++n)
+                    if (r + 8 * n < rows)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) to[8 * i + sv0] = to[8 * i + sv1] = -INFINITY;
-                }
+                        for (int i = 0; i < 4; ++i)
+                            sc[8 * n * p.stride + 8 * i + sv0] = sc[8 * n * p.stride + 8 * i + sv1] = -INFINITY;
+            take(false);
+            issue();
+            take(false);
+            issue();
         }
         if (w.tile == w.nt - 1 || it == tiles - 1) {   // the unit, or its part in this range, ends
             bool whole;
             const int slot = paged_part(p, w, t0, at + it, whole);
             if (w.n < 0) {
-                if (w.u == 0 && tid == 0) report(kStatusCheck);
+                if (w.h == 0 && w.sub == 0 && tid == 0) report(kStatusCheck);
             } else {
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
-                    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
-                    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+                    l[n] += __shfl_xor_sync(ALL, l[n], 1);
+                    l[n] += __shfl_xor_sync(ALL, l[n], 2);
                     if (cq == 0) mls[warp * kPagedRows + r + 8 * n] = make_float2(m[n], l[n]);
                 }
 #pragma unroll
@@ -717,7 +775,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                     paged_merge<T, DV>(p, w, obuf, mls, 8 * n, rows, whole, slot);
                     __syncthreads();
                 }
-                if (p.k && sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
+                if (p.k && w.sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
             }
         }
         if (it < tiles - 1) w.next(p);
@@ -804,15 +862,18 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
     __syncthreads();
 
     PagedWalk lw = w;
-    int issued = 0, page = paged_entry(p, lw, warp, lane);
+    // slot of this lane (lanes 0..15) in the tile whose loads are next
+    auto slot_in = [&]() { return lane < 16 ? (lw.tile << 6) + warp * 16 + lane : INT_MAX; };
+    auto entry = [&]() { return paged_entry(p, lw, slot_in()); };
+    int issued = 0, page = entry();
     auto issue = [&]() {
         if (issued < tiles) {
-            const int stage = issued % Cfg::ST, h = lw.u / p.nsub;
-            const int row = paged_entry_row(p, lw, warp, lane, page);
+            const int stage = issued % Cfg::ST;
+            const int row = paged_entry_row(p, lw, slot_in(), page);
             const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);
             if (lane == 0) masks[stage] = mask;
             if (mask) {
-                const size_t bh = (size_t)lw.b * c.Hkv + h;
+                const size_t bh = lw.bh(p);
                 const uint32_t dst = ring + stage * Cfg::STAGE;
                 const T *kn = (const T *)p.k + bh * c.dqk, *vn = (const T *)p.v + bh * c.dv;
 #pragma unroll
@@ -834,7 +895,7 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
             }
             if (++issued < tiles) {
                 lw.next(p);
-                page = paged_entry(p, lw, warp, lane);
+                page = entry();
             }
         }
         cp_async_commit();
@@ -846,8 +907,8 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
     float m[GM], l[GM];
     int t0 = 0;
     for (int it = 0; it < tiles; ++it) {
-        const int h = w.u / p.nsub, sub = w.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
-        const size_t hq0 = (size_t)w.b * p.Hq + h * p.g + sub * p.gs;
+        const int rows = w.rows(p);
+        const size_t hq0 = w.hq(p);
         if (it == 0 || w.tile == 0) {
             t0 = w.tile;
             __syncthreads();   // the queries of the last unit are read
@@ -899,14 +960,14 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
                     s[i][n] = x = mask >> (i * 8 + r) & 1 ? x : -INFINITY;
                     mx = fmaxf(mx, x);
                     if (p.scores && cq == 0)
-                        p.scores[(hq0 + n) * p.stride + w.tile * kPagedTile + warp * 16 + i * 8 + r] = x;
+                        p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + r] = x;
                 }
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 const float base = mx == -INFINITY ? 0.f : mx;
-                al[n] = exp2f(m[n] - base);
+                al[n] = ex2(m[n] - base);
                 m[n] = mx;
-                const float e0 = exp2f(s[0][n] - base), e1 = exp2f(s[1][n] - base);
+                const float e0 = ex2(s[0][n] - base), e1 = ex2(s[1][n] - base);
                 l[n] = l[n] * al[n] + e0 + e1;
                 if (cq == (n & 3)) {
                     ps[r * GM + n] = e0;
@@ -935,14 +996,14 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
         } else if (p.scores && w.n > 0 && cq == 0) {
             for (int n = 0; n < rows; ++n)
                 for (int i = 0; i < 2; ++i)
-                    p.scores[(hq0 + n) * p.stride + w.tile * kPagedTile + warp * 16 + i * 8 + r] = -INFINITY;
+                    p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + r] = -INFINITY;
         }
         __syncwarp();   // the weights are read before the next tile's
         if (w.tile == w.nt - 1 || it == tiles - 1) {
             bool whole;
             const int slot = paged_part(p, w, t0, at + it, whole);
             if (w.n < 0) {
-                if (w.u == 0 && tid == 0) report(kStatusCheck);
+                if (w.h == 0 && w.sub == 0 && tid == 0) report(kStatusCheck);
             } else {
 #pragma unroll
                 for (int n = 0; n < GM; ++n) {   // a slot's weight is held by its quad's four lanes alike
@@ -965,7 +1026,7 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
                     paged_merge<T, D>(p, w, obuf, mls, n0, min(rows, GM), whole, slot);
                     __syncthreads();
                 }
-                if (p.k && sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
+                if (p.k && w.sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
             }
         }
         if (it < tiles - 1) w.next(p);
@@ -980,31 +1041,33 @@ __device__ __forceinline__ float2 paged_part_ml(const PagedDecodeParams &p, int 
 }
 
 // Joins a unit's parts.  The K ranges that hold them share the work: their
-// blocks take equal slices of the unit's rows x dv outputs, and within a warp
-// a power of two of lanes shares one output's parts.
+// blocks take equal slices of the unit's rows x dv outputs, and KL neighbouring
+// lanes share one output's parts (as many as leave one output to each group, so
+// that the loads of a lane, one after the other, are few).
 template <typename T>
 __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const PagedSpan &s, long long chunk)
 {
     const int g0 = (int)(s.first / chunk), g1 = (int)((s.end - 1) / chunk), K = g1 - g0 + 1, dv = p.c.dv;
     const int h = s.u / p.nsub, sub = s.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
     const size_t hq0 = (size_t)s.b * p.Hq + h * p.g + sub * p.gs;
-    const int E = rows * dv, idx = blockIdx.x - g0;
-    const int e0 = (int)((long long)E * idx / K), e1 = (int)((long long)E * (idx + 1) / K);
+    const int E = rows * dv, per = (E + K - 1) / K, e0 = (blockIdx.x - g0) * per, e1 = min(E, e0 + per);
     int KL = 1;
-    while (KL < K && KL < 32) KL <<= 1;
-    const int sub_lane = threadIdx.x % KL;
+    while (KL < K && KL < 32 && per * KL * 2 <= kPagedThreads) KL <<= 1;
+    const int mine = threadIdx.x & (KL - 1);
     for (int base = e0; base < e1; base += kPagedThreads / KL) {   // the same count for every thread
         const int e = base + threadIdx.x / KL;
         const bool on = e < e1;
         const int row = on ? e / dv : 0, col = on ? e - row * dv : 0;
         float M = -INFINITY;
-        for (int i = sub_lane; i < K; i += KL) M = fmaxf(M, paged_part_ml(p, g0, i, row).x);
+#pragma unroll 8
+        for (int i = mine; i < K; i += KL) M = fmaxf(M, paged_part_ml(p, g0, i, row).x);
         for (int off = 1; off < KL; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
         const float b = M == -INFINITY ? 0.f : M;
         float L = 0.f, acc = 0.f;
-        for (int i = sub_lane; i < K; i += KL) {
+#pragma unroll 8
+        for (int i = mine; i < K; i += KL) {
             const float2 e2 = paged_part_ml(p, g0, i, row);
-            const float f = exp2f(e2.x - b);
+            const float f = ex2(e2.x - b);
             L = fmaf(f, e2.y, L);
             acc = fmaf(f, p.part[(((size_t)(g0 + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows + row) * dv + col], acc);
         }
@@ -1012,7 +1075,7 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
             L += __shfl_xor_sync(0xffffffffu, L, off);
             acc += __shfl_xor_sync(0xffffffffu, acc, off);
         }
-        if (on && sub_lane == 0) {
+        if (on && mine == 0) {
             const bool none = L == 0.f;
             st((T *)p.y + (hq0 + row) * dv + col, none ? 0.f : acc / L);
             if (col == 0 && p.lse) p.lse[hq0 + row] = none ? -INFINITY : M * 0.693147180559945309f + logf(L);
@@ -1036,15 +1099,15 @@ __global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedDe
     const int tid = threadIdx.x;
     PagedWalk w;
     w.b = rec.b;
-    w.u = rec.u;
+    w.h = rec.u / p.nsub;
+    w.sub = rec.u - w.h * p.nsub;
     w.tile = rec.tile;
     w.load(p);
     long long at = blockIdx.x * rec.chunk;
     for (int left = rec.tiles; left > 0;) {
         const int here = min(left, w.nt - w.tile);
-        if (w.u % p.nsub == 0 && w.n > 0) {
-            const int h = w.u / p.nsub;
-            const size_t hq0 = (size_t)w.b * p.Hq + h * p.g, bh = (size_t)w.b * c.Hkv + h;
+        if (w.sub == 0 && w.n > 0) {
+            const size_t hq0 = w.hq(p), bh = w.bh(p);
             __syncthreads();
             for (int j = tid; j < p.g; j += kPagedThreads) {
                 const int sub = j / p.gs;
@@ -1054,20 +1117,22 @@ __global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedDe
                     lse2[j] = p.lse2[hq0 + j];
                 } else {
                     float M = -INFINITY, L = 0.f;
+#pragma unroll 8
                     for (int i = 0; i <= g1 - g0; ++i) M = fmaxf(M, paged_part_ml(p, g0, i, j - sub * p.gs).x);
+#pragma unroll 8
                     for (int i = 0; i <= g1 - g0; ++i) {
                         const float2 e = paged_part_ml(p, g0, i, j - sub * p.gs);
-                        L = fmaf(exp2f(e.x - (M == -INFINITY ? 0.f : M)), e.y, L);
+                        L = fmaf(ex2(e.x - (M == -INFINITY ? 0.f : M)), e.y, L);
                     }
                     lse2[j] = L == 0.f ? -INFINITY : M + log2f(L);
                 }
             }
             __syncthreads();
-            const int end = min(w.n, (w.tile + here) * kPagedTile);
-            for (int t = w.tile * kPagedTile + tid; t < end; t += kPagedThreads) {
+            const int end = min((long long)w.n, (long long)(w.tile + here) << p.tile);
+            for (int t = (w.tile << p.tile) + tid; t < end; t += kPagedThreads) {
                 float sum = 0.f;
                 for (int j = 0; j < p.g; ++j)
-                    if (lse2[j] != -INFINITY) sum += exp2f(p.scores[(hq0 + j) * p.stride + t] - lse2[j]);
+                    if (lse2[j] != -INFINITY) sum += ex2(p.scores[(hq0 + j) * p.stride + t] - lse2[j]);
                 const size_t to = bh * c.cap() + t;
                 p.w_out[to] = (p.k && t == w.n - 1 ? 0.f : p.w_in[to]) + sum;
             }
