@@ -108,18 +108,22 @@ la_status launch_status()
 // each of these kernels waits for the previous one to complete (its writes
 // visible) before it touches global memory.
 template <typename... KArgs, typename... Args>
-la_status launch_pdl(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream, Args &&...args)
+la_status launch_pdl_cluster(void (*kernel)(KArgs...), int grid, int threads, int smem, int cluster, cudaStream_t stream,
+                             Args &&...args)
 {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     if (e == cudaSuccess) return LA_OK;
 #ifdef LA_DEBUG_LAUNCH
@@ -127,6 +131,12 @@ la_status launch_pdl(void (*kernel)(KArgs...), int grid, int threads, int smem, 
 #endif
     (void)cudaGetLastError();   // consume it, as launch_status does for the other launches
     return LA_ERR_CUDA;
+}
+
+template <typename... KArgs, typename... Args>
+la_status launch_pdl(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream, Args &&...args)
+{
+    return launch_pdl_cluster(kernel, grid, threads, smem, 1, stream, std::forward<Args>(args)...);
 }
 
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device) and
@@ -656,7 +666,7 @@ static la_status check_paged(int B, int Hq, int Hkv, int dqk, int dv, int num_pa
     if (Hq % Hkv) return LA_ERR_INVALID_ARG;
     const int64_t lim = (int64_t)1 << 31;
     if ((int64_t)num_pages * Hkv >= lim || (int64_t)num_pages * Hkv * page_size >= lim) return LA_ERR_INVALID_ARG;
-    if ((int64_t)max_pages * page_size >= lim) return LA_ERR_INVALID_ARG;
+    if ((int64_t)max_pages * page_size >= lim / 2) return LA_ERR_INVALID_ARG;   // room above a slot's index
     if ((int64_t)B * Hq * (dqk > dv ? dqk : dv) >= lim) return LA_ERR_INVALID_ARG;
     if (dqk > 128 || dv > 128) return LA_ERR_UNSUPPORTED;
     return LA_OK;
@@ -1354,8 +1364,8 @@ static int64_t evict_maxmoves(int page_size, int max_pages, int budget)
 size_t la_paged_evict_workspace_bytes(int B, int Hkv, int page_size, int max_pages, int budget)
 {
     if (check_paged(B, Hkv, Hkv, 1, 1, 1, page_size, max_pages, LA_F32) != LA_OK || budget < 1) return 0;
-    // the slots that move, from and to; their number per (b, h); the new lengths
-    return ((size_t)B * Hkv * (2 * evict_maxmoves(page_size, max_pages, budget) + 1) + B) * sizeof(int);
+    // the slots that move, to and from; the new lengths
+    return ((size_t)B * Hkv * 2 * evict_maxmoves(page_size, max_pages, budget) + B) * sizeof(int);
 }
 
 la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_table, const int32_t *lens,
@@ -1395,16 +1405,24 @@ la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_tabl
     p.maxmoves = (int)evict_maxmoves(page_size, max_pages, budget);
     p.holes = (int *)workspace;
     p.movers = p.holes + (size_t)B * Hkv * p.maxmoves;
-    p.count = p.movers + (size_t)B * Hkv * p.maxmoves;
-    p.newlen = p.count + (size_t)B * Hkv;
-    p.vec_k = rows16(dqk, dtype);
-    p.vec_v = rows16(dv, dtype);
+    p.newlen = lens_out == lens ? p.movers + (size_t)B * Hkv * p.maxmoves : nullptr;
+    p.elem = (int)elem_size(dtype);
+    p.width = rows16(dqk, dtype) && rows16(dv, dtype) ? 16 : p.elem;
+    // blocks per (b, h): as many as keep about two blocks on every SM busy, with
+    // at least 1024 slots each
+    const int64_t units = (int64_t)B * Hkv, cap = (int64_t)max_pages * page_size;
+    int cs = 1;
+    while (cs < kEvictMaxCluster && units * cs * 2 <= 2 * kNumSms && cap >= (int64_t)cs * 2 * 1024) cs *= 2;
+    if (units * cs >= (int64_t)1 << 31) return LA_ERR_INVALID_ARG;
+    const int64_t slice = (cap + cs * kEvictThreads - 1) / (cs * kEvictThreads) * kEvictThreads;
+    p.keys = (int)(slice < kEvictMaxKeys ? slice : kEvictMaxKeys);
     cudaStream_t st = (cudaStream_t)stream;
-    const la_status s1 = launch_pdl(paged_evict_select_kernel, B * Hkv, kEvictThreads, 0, st, p);
-    if (s1 != LA_OK) return s1;
-    const int splits = 1;
-    if (dtype == LA_F32) return launch_pdl(paged_evict_move_kernel<float>, B * Hkv * splits, 256, 0, st, p, splits);
-    return launch_pdl(paged_evict_move_kernel<__nv_bfloat16>, B * Hkv * splits, 256, 0, st, p, splits);
+    const size_t smem = p.keys * sizeof(uint32_t);
+    // the kernel's static shared memory (below 20 KB) counts towards the 48 KB that need no asking
+    if (set_smem<paged_evict_kernel>(smem + 20 * 1024) != LA_OK) return LA_ERR_CUDA;
+    const la_status s1 = launch_pdl_cluster(paged_evict_kernel, (int)(units * cs), kEvictThreads, (int)smem, cs, st, p);
+    if (s1 != LA_OK || !p.newlen) return s1;
+    return launch_pdl(paged_evict_lens_kernel, (B + 255) / 256, 256, 0, st, p);
 }
 
 int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
@@ -1417,7 +1435,7 @@ int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int pa
     PagedPlan pl;
     if (op == 1 && paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl) != LA_OK) return -1;
     const char *nm = op == 0   ? "paged_fill_kernel"
-                     : op == 2 ? "paged_evict_select_kernel,paged_evict_move_kernel"
+                     : op == 2 ? "paged_evict_kernel,paged_evict_lens_kernel"
                      : pl.mma  ? "paged_decode_mma_kernel,paged_join_kernel"
                                : "paged_decode_simt_kernel,paged_join_kernel";
     if (buf && buflen) {

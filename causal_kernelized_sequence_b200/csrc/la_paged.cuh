@@ -3,6 +3,7 @@
 // eviction by accumulated attention weight.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <limits.h>
 #include <type_traits>
 
@@ -1058,22 +1059,41 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
         const int e = base + threadIdx.x / KL;
         const bool on = e < e1;
         const int row = on ? e / dv : 0, col = on ? e - row * dv : 0;
-        float M = -INFINITY;
-#pragma unroll 8
-        for (int i = mine; i < K; i += KL) M = fmaxf(M, paged_part_ml(p, g0, i, row).x);
-        for (int off = 1; off < KL; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        const float b = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc = 0.f;
-#pragma unroll 8
-        for (int i = mine; i < K; i += KL) {
-            const float2 e2 = paged_part_ml(p, g0, i, row);
-            const float f = ex2(e2.x - b);
-            L = fmaf(f, e2.y, L);
-            acc = fmaf(f, p.part[(((size_t)(g0 + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows + row) * dv + col], acc);
+        // one pass: maximum, sum and accumulator of eight parts at a time
+        float M = -INFINITY, L = 0.f, acc = 0.f;
+        for (int i0 = mine; i0 < K; i0 += 8 * KL) {
+            float2 ml[8];
+            float x[8], mx = M;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * KL;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                x[j] = 0.f;
+                if (i < K) {
+                    ml[j] = paged_part_ml(p, g0, i, row);
+                    x[j] = p.part[(((size_t)(g0 + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows + row) * dv + col];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mx = fmaxf(mx, ml[j].x);
+            const float base = mx == -INFINITY ? 0.f : mx, f = ex2(M - base);
+            L *= f;
+            acc *= f;
+            M = mx;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = ex2(ml[j].x - base);
+                L = fmaf(e, ml[j].y, L);
+                acc = fmaf(e, x[j], acc);
+            }
         }
         for (int off = 1; off < KL; off <<= 1) {
-            L += __shfl_xor_sync(0xffffffffu, L, off);
-            acc += __shfl_xor_sync(0xffffffffu, acc, off);
+            const float m2 = __shfl_xor_sync(0xffffffffu, M, off), l2 = __shfl_xor_sync(0xffffffffu, L, off);
+            const float a2 = __shfl_xor_sync(0xffffffffu, acc, off), mx = fmaxf(M, m2);
+            const float base = mx == -INFINITY ? 0.f : mx, f = ex2(M - base), f2 = ex2(m2 - base);
+            L = L * f + l2 * f2;
+            acc = acc * f + a2 * f2;
+            M = mx;
         }
         if (on && mine == 0) {
             const bool none = L == 0.f;
@@ -1157,15 +1177,21 @@ struct PagedEvictParams {
     int *pos_out;
     const int *pos;
     int *holes, *movers;   // [B*Hkv, maxmoves] each
-    int *count, *newlen;   // [B*Hkv], [B]
+    int *newlen;           // [B]; null: lens_out is written by the first kernel
     int budget, recent, maxmoves;
-    bool vec_k, vec_v;
+    int elem;              // bytes of an element
+    int width;             // bytes a row copy moves at once: 16 if both rows allow it, else an element
+    int keys;              // keys that fit the block's shared memory
 };
 
 constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictBins = 2048;
+constexpr int kEvictMaxKeys = 12288;
+constexpr int kEvictMaxCluster = 8;
 
 // Weight as an unsigned key of the same order: larger weight, larger key; NaN
-// counts as -inf and -0 as +0.
+// counts as -inf and -0 as +0.  No weight has the key 0 or 2^32 - 1.
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
     if (!(w == w)) w = -INFINITY;
@@ -1173,129 +1199,257 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One block per (b, h): a radix select over the weights' keys (four passes of
-// 8 bits) finds the smallest key that is kept, then one pass in slot order
-// lists the dropped slots below the budget and the kept ones above it, and
-// moves their weights and positions.
-__global__ void __launch_bounds__(kEvictThreads) paged_evict_select_kernel(const PagedEvictParams p)
+// Copies the moved rows of this block's share of the list, eight lanes to a
+// row pair, four pieces in flight per lane.
+template <typename V>
+__device__ __forceinline__ void evict_rows(const PagedEvictParams &p, int b, int h, const int *holes,
+                                           const int *movers, int m, int rank, int blocks)
 {
+    constexpr int G = 8;
+    const PagedCache &c = p.c;
+    const int pk = c.dqk * p.elem / (int)sizeof(V), pv = c.dv * p.elem / (int)sizeof(V), np = pk + pv;
+    const int lane = threadIdx.x % G, step = blocks * (kEvictThreads / G);
+    V *kp = (V *)c.kp, *vp = (V *)c.vp;
+    for (int i = rank * (kEvictThreads / G) + threadIdx.x / G; i < m; i += step) {
+        const size_t to = paged_row(c, b, h, holes[i]), from = paged_row(c, b, h, movers[i]);
+        for (int q = lane; q < np; q += 4 * G) {
+            V x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = q + j * G;
+                if (at < np) x[j] = at < pk ? kp[from * pk + at] : vp[from * pv + at - pk];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = q + j * G;
+                if (at < pk) kp[to * pk + at] = x[j];
+                else if (at < np) vp[to * pv + at - pk] = x[j];
+            }
+        }
+    }
+}
+
+// One cluster of blocks per (b, h), each block with a slice of the slots.  The
+// order is one of 32-bit keys: a recent token's is the largest, the others
+// follow their weights.  A radix select (11, 11 and 10 bits; the blocks add
+// their histograms over distributed shared memory) finds the smallest key that
+// is kept and how many slots of that key are; sweeps in slot order then rank
+// the ties, list the dropped slots below the budget and the kept ones above it,
+// and move rows, weights and positions along the two lists.  Sources lie at or
+// above the budget and destinations below it, so moves need no order.
+__global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(const PagedEvictParams p)
+{
+    extern __shared__ __align__(16) int evict_smem[];
+    __shared__ int hist[2][kEvictBins], part[kEvictWarps], pick[3];
+    __shared__ int xch[4];   // read by the cluster's other blocks
+    namespace cg = cooperative_groups;
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
-    __shared__ int hist[256], part[kEvictThreads / 32], pick[2];
+    cg::cluster_group cl = cg::this_cluster();
+    const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const PagedCache &c = p.c;
-    const int tid = threadIdx.x;
-    const size_t bh = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const size_t bh = blockIdx.x / CS;
     const int b = (int)(bh / c.Hkv), h = (int)(bh - (size_t)b * c.Hkv);
     const int n = c.lens[b], budget = p.budget;
-    const long long last = p.recent ? p.pos[b] : 0;
-    bool bad = n < 0 || n > c.cap() || last < 0;
-    if (!bad && n > budget) {
-        const int used = (n - 1) / c.page + 1;
-        for (int i = tid; i < used; i += kEvictThreads)
-            if ((unsigned)c.table[(size_t)b * c.max_pages + i] >= (unsigned)c.num_pages) bad = true;
-    }
-    bad = __syncthreads_or(bad);
-    if (tid == 0) {
-        if (bad) report(kStatusCheck);
-        if (h == 0) p.newlen[b] = bad ? n : min(n, budget);
-        if (bad || n <= budget) p.count[bh] = 0;
-    }
-    if (bad) return;
+    const long long last = p.recent ? (long long)p.pos[b] : 0;
     const float *w = p.w_in + bh * c.cap();
     float *wo = p.w_out + bh * c.cap();
     const int *ps = p.pos_in ? p.pos_in + bh * c.cap() : nullptr;
     int *po = p.pos_out ? p.pos_out + bh * c.cap() : nullptr;
-    if (n <= budget) {
-        for (int t = tid; t < n; t += kEvictThreads) {
-            if (wo != w) wo[t] = w[t];
-            if (po != ps) po[t] = ps[t];
-        }
+    const bool first = rank == 0 && h == 0 && tid == 0;   // writes the sequence's length
+    int *const len_to = p.newlen ? p.newlen : p.lens_out;
+
+    // every block of a cluster sees the same n, so all of them leave here or none
+    if (n < 0 || n > c.cap() || last < 0 || n <= budget) {
+        const bool bad = n < 0 || n > c.cap() || last < 0;
+        if (bad && rank == 0 && tid == 0) report(kStatusCheck);
+        if (first && (!bad || p.newlen)) len_to[b] = n;
+        if (!bad)
+            for (int t = rank * kEvictThreads + tid; t < n; t += CS * kEvictThreads) {
+                if (wo != w) wo[t] = w[t];
+                if (po != ps) po[t] = ps[t];
+            }
         return;
     }
-    auto recent = [&](int t) { return p.recent && ps[t] >= last - p.recent; };
-    // the class the cut falls into: the recent tokens if they alone exceed the
-    // budget (then the others are all dropped), else the others (the recent all stay)
-    int nrec = 0;
-    for (int t = tid; t < n; t += kEvictThreads) nrec += recent(t);
+
+    // slots [s0, s1) of this block, a whole number of 32 per warp: [a0, a1)
+    const int per = (n + CS * kEvictThreads - 1) / (CS * kEvictThreads) * kEvictThreads;
+    const int s0 = min(n, rank * per), s1 = min(n, s0 + per);
+    const int a0 = s0 + warp * (per / kEvictWarps), a1 = min(s1, a0 + per / kEvictWarps);
+    uint32_t *keys = reinterpret_cast<uint32_t *>(evict_smem);
+    const bool cached = per <= p.keys;
+    auto is_recent = [&](int t) { return p.recent && ps[t] >= last - p.recent; };
+    // if the recent tokens alone exceed the budget, their weights decide and the others' keys are 0
+    bool crowded = false;
+    auto make_key = [&](int t) {
+        const bool late = is_recent(t);
+        if (crowded) return late ? weight_key(w[t]) : 0u;
+        return late ? 0xffffffffu : weight_key(w[t]);
+    };
+    auto key_of = [&](int t) { return cached ? keys[t - s0] : make_key(t); };
+    // the sum over the cluster's blocks of a value held by thread 0 of each, in `slot`
+    // of xch; also the sum over the blocks before this one.  One barrier each.
+    auto exchange = [&](int slot, int value, int &before) {
+        if (tid == 0) xch[slot] = value;
+        cl.sync();
+        int total = 0;
+        before = 0;
+        for (int i = 0; i < CS; ++i) {
+            const int x = *cl.map_shared_rank(&xch[slot], i);
+            if (i < rank) before += x;
+            total += x;
+        }
+        return total;
+    };
+
+    // keys, the number of recent tokens, and the table's entries
+    for (int i = tid; i < 2 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+    bool bad = false;
+    const int used = (n - 1) / c.page + 1;
+    for (int i = rank * kEvictThreads + tid; i < used; i += CS * kEvictThreads)
+        if ((unsigned)c.table[(size_t)b * c.max_pages + i] >= (unsigned)c.num_pages) bad = true;
+    int late = 0, none;
+    for (int t = a0 + lane; t < a1; t += 32) {
+        const uint32_t key = make_key(t);
+        if (cached) keys[t - s0] = key;
+        late += key == 0xffffffffu;
+    }
+    bad = __syncthreads_or(bad);
     int total;
-    (void)block_scan<kEvictThreads>(nrec, part, total);
-    const bool cls = total >= budget;
-    int need = cls ? budget : budget - total;
+    (void)block_scan<kEvictThreads>(late, part, total);
+    // (a bad table in bit 30: there are fewer than 2^30 recent tokens, or it does not matter which)
+    late = exchange(0, bad ? 1 << 30 : min(total, 1 << 26), none);
+    if (late >= 1 << 30) {
+        if (rank == 0 && tid == 0) report(kStatusCheck);
+        if (first && p.newlen) len_to[b] = n;
+        cl.sync();   // no block leaves while another reads its xch
+        return;
+    }
+    if (late > budget) {
+        crowded = true;
+        if (cached)
+            for (int t = a0 + lane; t < a1; t += 32) keys[t - s0] = make_key(t);
+        __syncthreads();
+    }
+
+    // the radix select, from the top
     uint32_t thr = 0, known = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        __syncthreads();
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int t = tid; t < n; t += kEvictThreads)
-            if (recent(t) == cls) {
-                const uint32_t key = weight_key(w[t]);
-                if ((key & known) == thr) atomicAdd(&hist[key >> shift & 255], 1);
-            }
-        __syncthreads();
-        if (tid == 0) {
-            int bin = 255, left = need;
-            while (hist[bin] < left) left -= hist[bin--];   // the counts add up to at least `need`
-            pick[0] = bin;
+    int need = budget, ties = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        int *hs = hist[pass & 1];
+        if (pass == 2) {   // (the other blocks have read it: they have passed the barrier of pass 1)
+            for (int i = tid; i < kEvictBins; i += kEvictThreads) hs[i] = 0;
+            __syncthreads();
+        }
+        for (int t = a0 + lane; t < a1; t += 32) {
+            const uint32_t key = key_of(t);
+            if ((key & known) == thr) atomicAdd(&hs[key >> shift & ((1u << bits) - 1)], 1);
+        }
+        cl.sync();
+        // thread i owns the four bins from 4 (511 - i) on: larger keys first
+        int4 sum = make_int4(0, 0, 0, 0);
+        const int bin = kEvictBins - 4 - 4 * tid;
+        for (int i = 0; i < CS; ++i) {
+            const int4 x = *reinterpret_cast<const int4 *>(cl.map_shared_rank(hs, i) + bin);
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
+        }
+        const int mine = sum.x + sum.y + sum.z + sum.w;
+        int left = need - block_scan<kEvictThreads>(mine, part, total);
+        if (left > 0 && left <= mine) {   // one thread: the bins add up to at least `need`
+            int at = bin + 3, size = sum.w;
+            if (left > size) left -= size, at = bin + 2, size = sum.z;
+            if (at == bin + 2 && left > size) left -= size, at = bin + 1, size = sum.y;
+            if (at == bin + 1 && left > size) left -= size, at = bin, size = sum.x;
+            pick[0] = at;
             pick[1] = left;
+            pick[2] = size;
         }
         __syncthreads();
         thr |= (uint32_t)pick[0] << shift;
-        known |= 255u << shift;
+        known |= ((1u << bits) - 1) << shift;
         need = pick[1];
+        ties = pick[2];
     }
-    // slot order: `need` slots with key == thr stay, the lowest ones
-    int ties = 0, nh = 0, nm = 0;
-    int *holes = p.holes + bh * p.maxmoves, *movers = p.movers + bh * p.maxmoves;
-    for (int t0 = 0; t0 < n; t0 += kEvictThreads) {
-        const int t = t0 + tid;
-        const bool in = t < n, r = in && recent(t);
-        const uint32_t key = in && r == cls ? weight_key(w[t]) : 0;
-        const bool eq = in && r == cls && key == thr;
-        const int rank = ties + block_scan<kEvictThreads>((int)eq, part, total);
-        ties += total;
-        const bool keep = in && (r == cls ? key > thr || (eq && rank < need) : r);
-        const bool hole = in && t < budget && !keep, mover = keep && t >= budget;
-        const int ih = nh + block_scan<kEvictThreads>((int)hole, part, total);
-        nh += total;
-        const int im = nm + block_scan<kEvictThreads>((int)mover, part, total);
-        nm += total;
-        if (hole) holes[ih] = t;
-        if (mover) movers[im] = t;
-        if (keep && !mover) {
-            if (wo != w) wo[t] = w[t];
-            if (po != ps) po[t] = ps[t];
+
+    // `need` of the `ties` slots with key == thr stay, the lowest ones
+    int rank0 = 0;   // ties before this warp's slots
+    if (need < ties) {
+        int mine = 0;
+        for (int t = a0; t < a1; t += 32) mine += __popc(__ballot_sync(0xffffffffu, t + lane < a1 && key_of(t + lane) == thr));
+        const int before = block_scan<kEvictThreads>(lane == 0 ? mine : 0, part, total);
+        int blocks_before;
+        (void)exchange(1, total, blocks_before);
+        rank0 = blocks_before + __shfl_sync(0xffffffffu, before, 0);
+    }
+    // slots t0 .. t0 + 31 of this warp: which are kept
+    int seen;
+    auto kept = [&](int t0) {
+        const bool in = t0 + lane < a1;
+        const uint32_t key = in ? key_of(t0 + lane) : 0;
+        bool eq = in && key == thr;
+        if (need < ties) {
+            const uint32_t all = __ballot_sync(0xffffffffu, eq);
+            eq = eq && rank0 + seen + __popc(all & ((1u << lane) - 1)) < need;
+            seen += __popc(all);
         }
+        return __ballot_sync(0xffffffffu, in && (key > thr || eq));
+    };
+    // among slots t0 .. t0 + 31, those below the budget, and those that exist
+    auto below = [&](int t0) { return t0 + 32 <= budget ? 0xffffffffu : t0 >= budget ? 0u : (1u << (budget - t0)) - 1; };
+    auto exist = [&](int t0) { return t0 + 32 <= a1 ? 0xffffffffu : (1u << (a1 - t0)) - 1; };
+    int nh = 0, nm = 0;
+    seen = 0;
+    for (int t = a0; t < a1; t += 32) {
+        const uint32_t k = kept(t), lo = below(t);
+        nh += __popc(~k & lo & exist(t));
+        nm += __popc(k & ~lo);
     }
-    __syncthreads();   // the lists are complete and visible to the block
-    for (int i = tid; i < nm; i += kEvictThreads) {
-        wo[holes[i]] = w[movers[i]];
-        if (po) po[holes[i]] = ps[movers[i]];
+    int ih = block_scan<kEvictThreads>(lane == 0 ? nh : 0, part, total), blocks_before;
+    ih = __shfl_sync(0xffffffffu, ih, 0);
+    const int m = exchange(2, total, blocks_before);
+    ih += blocks_before;
+    int im = block_scan<kEvictThreads>(lane == 0 ? nm : 0, part, total);
+    im = __shfl_sync(0xffffffffu, im, 0);
+    (void)exchange(3, total, blocks_before);
+    im += blocks_before;
+    int *holes = p.holes + bh * p.maxmoves, *movers = p.movers + bh * p.maxmoves;
+    seen = 0;
+    for (int t = a0; t < a1; t += 32) {
+        const uint32_t k = kept(t), lo = below(t), hole = ~k & lo & exist(t), mover = k & ~lo;
+        const uint32_t before = (1u << lane) - 1;
+        if (hole >> lane & 1) holes[ih + __popc(hole & before)] = t + lane;
+        if (mover >> lane & 1) movers[im + __popc(mover & before)] = t + lane;
+        if (k & lo & (1u << lane)) {
+            if (wo != w) wo[t + lane] = w[t + lane];
+            if (po != ps) po[t + lane] = ps[t + lane];
+        }
+        ih += __popc(hole);
+        im += __popc(mover);
     }
-    if (tid == 0) p.count[bh] = nm;
+    cl.sync();   // the lists are complete, all keys are read, and no block reads another's memory any more
+    for (int i = rank * kEvictThreads + tid; i < m; i += CS * kEvictThreads) {
+        const int to = holes[i], from = movers[i];
+        wo[to] = w[from];
+        if (po) po[to] = ps[from];
+    }
+    if (first) len_to[b] = budget;
+    if (p.width == 16) evict_rows<uint4>(p, b, h, holes, movers, m, rank, CS);
+    else if (p.width == 4) evict_rows<uint32_t>(p, b, h, holes, movers, m, rank, CS);
+    else evict_rows<uint16_t>(p, b, h, holes, movers, m, rank, CS);
 }
 
-// Copies the moved rows; the sources lie at or above the budget and the
-// destinations below it, so no order is needed.  The first blocks write lens.
-template <typename T>
-__global__ void __launch_bounds__(256) paged_evict_move_kernel(const PagedEvictParams p, int splits)
+// lens in place: no block of the kernel above may still read it when it is written.
+__global__ void paged_evict_lens_kernel(const PagedEvictParams p)
 {
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
-    const PagedCache &c = p.c;
-    const size_t bh = blockIdx.x / splits;
-    const int s = (int)(blockIdx.x - bh * splits);
-    const int b = (int)(bh / c.Hkv), h = (int)(bh - (size_t)b * c.Hkv);
-    if (h == 0 && s == 0 && threadIdx.x == 0) p.lens_out[b] = p.newlen[b];
-    const int m = p.count[bh];
-    constexpr int G = 8;
-    const int lane = threadIdx.x % G;
-    for (int i = s * (256 / G) + threadIdx.x / G; i < m; i += splits * (256 / G)) {
-        const int to = paged_row(c, b, h, p.holes[bh * p.maxmoves + i]);
-        const int from = paged_row(c, b, h, p.movers[bh * p.maxmoves + i]);
-        T *kp = (T *)c.kp, *vp = (T *)c.vp;
-        copy_row<T, G>(kp + (size_t)to * c.dqk, kp + (size_t)from * c.dqk, c.dqk, p.vec_k, lane);
-        copy_row<T, G>(vp + (size_t)to * c.dv, vp + (size_t)from * c.dv, c.dv, p.vec_v, lane);
-    }
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b < p.c.B) p.lens_out[b] = p.newlen[b];
 }
 
 }  // namespace la

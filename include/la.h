@@ -347,7 +347,8 @@ LA_API la_status la_swa_decode_step(const void *q, const void *k, const void *v,
  * slots that a call writes must belong to one sequence.
  *
  * Sizes: dqk, dv in [1,128]; any page_size >= 1; num_pages * Hkv * page_size
- * and max_pages * page_size below 2^31 (element offsets are 64 bits wide).
+ * below 2^31, max_pages * page_size below 2^30 (element offsets are 64 bits
+ * wide).
  * What lies in device memory is checked there: a sequence with lens[b] < 0,
  * more slots than its table holds, or pos[b] < 0 where pos is used, is left
  * as it was (its outputs are not written either) and sets LA_ERR_DEVICE_CHECK
@@ -436,8 +437,9 @@ LA_API la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *blo
                                 void *stream);
 
 /* la_kernel_plan for the paged calls: op 0 = la_paged_cache_fill, 1 =
- * la_paged_decode_step, 2 = la_paged_evict (Hq ignored in 0 and 2).  Same
- * output rules. */
+ * la_paged_decode_step, 2 = la_paged_evict in place (Hq ignored in 0 and 2;
+ * with another lens_out its second kernel is not launched).  Same output
+ * rules. */
 LA_API int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
                                 int with_weights, int dtype, char *buf, size_t buflen);
 

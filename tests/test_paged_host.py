@@ -40,7 +40,8 @@ def _evict(lib, kp=0x1000, vp=0x2000, tab=0x3000, lens=0x4000, lo=0x4000, wi=0x1
 
 
 SIZES = [dict(B=0), dict(Hkv=0), dict(dqk=0), dict(dv=-1), dict(num=0), dict(page=0), dict(mp=0), dict(dt=2),
-         dict(num=1 << 20, page=1 << 11, Hkv=2, Hq=2), dict(page=1 << 16, mp=1 << 15, num=1)]
+         dict(num=1 << 20, page=1 << 11, Hkv=2, Hq=2), dict(page=1 << 16, mp=1 << 15, num=1),
+         dict(page=1 << 15, mp=1 << 15, num=1)]
 MISALIGNED = [dict(kp=0x5008), dict(vp=0x6004), dict(tab=0x7002), dict(lens=0x8001), dict(kp=None), dict(vp=None),
               dict(tab=None), dict(lens=None)]
 
@@ -87,9 +88,9 @@ def test_evict_arguments_refused(lib):
 
 def test_workspace_bytes(lib):
     f = la.la_paged_evict_workspace_bytes
-    assert f(2, 3, 16, 4, 32) == (6 * (2 * 32 + 1) + 2) * 4          # 64 slots, half of them move at most
-    assert f(2, 3, 16, 4, 60) == (6 * (2 * 4 + 1) + 2) * 4
-    assert f(2, 3, 16, 4, 100) == (6 + 2) * 4                        # nothing can move
+    assert f(2, 3, 16, 4, 32) == (6 * 2 * 32 + 2) * 4                # 64 slots, half of them move at most
+    assert f(2, 3, 16, 4, 60) == (6 * 2 * 4 + 2) * 4
+    assert f(2, 3, 16, 4, 100) == 2 * 4                              # nothing can move
     assert f(0, 3, 16, 4, 32) == 0 and f(2, 3, 16, 4, 0) == 0
     assert la.la_paged_decode_workspace_bytes(2, 3, 2, 64, 64, 16, 4, False, la.LA_BF16) == 0      # 3 heads over 2
 
