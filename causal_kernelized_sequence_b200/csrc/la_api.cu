@@ -793,6 +793,16 @@ static la_status paged_simt(const PagedDecodeParams &p, const PagedPlan &pl, cud
     return pl.gs <= 4 ? paged_simt_run<T, 128, 4>(p, pl, st) : paged_simt_run<T, 128, 16>(p, pl, st);
 }
 
+// The eviction with U row pairs in flight per warp, BLOCKS blocks on an SM.
+template <int U, int BLOCKS, bool CLUSTER>
+static la_status paged_evict_run(const PagedEvictParams &p, int grid, int cluster, cudaStream_t st)
+{
+    const size_t smem = p.keys * sizeof(uint32_t);
+    // the kernel's static shared memory (below 20 KB) counts towards the 48 KB that need no asking
+    if (set_smem<paged_evict_kernel<U, BLOCKS, CLUSTER>>(smem + 20 * 1024) != LA_OK) return LA_ERR_CUDA;
+    return launch_pdl_cluster(paged_evict_kernel<U, BLOCKS, CLUSTER>, grid, kEvictThreads, (int)smem, cluster, st, p);
+}
+
 extern "C" {
 
 int la_version(void) { return 100; }
@@ -1408,19 +1418,17 @@ la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_tabl
     p.newlen = lens_out == lens ? p.movers + (size_t)B * Hkv * p.maxmoves : nullptr;
     p.elem = (int)elem_size(dtype);
     p.width = rows16(dqk, dtype) && rows16(dv, dtype) ? 16 : p.elem;
-    // blocks per (b, h): as many as keep about two blocks on every SM busy, with
+    // blocks per (b, h): as many as run at once (four on an SM), with
     // at least 1024 slots each
     const int64_t units = (int64_t)B * Hkv, cap = (int64_t)max_pages * page_size;
     int cs = 1;
-    while (cs < kEvictMaxCluster && units * cs * 2 <= 2 * kNumSms && cap >= (int64_t)cs * 2 * 1024) cs *= 2;
+    while (cs < kEvictMaxCluster && units * cs * 2 <= 4 * kNumSms && cap >= (int64_t)cs * 2 * 1024) cs *= 2;
     if (units * cs >= (int64_t)1 << 31) return LA_ERR_INVALID_ARG;
     const int64_t slice = (cap + cs * kEvictThreads - 1) / (cs * kEvictThreads) * kEvictThreads;
     p.keys = (int)(slice < kEvictMaxKeys ? slice : kEvictMaxKeys);
     cudaStream_t st = (cudaStream_t)stream;
-    const size_t smem = p.keys * sizeof(uint32_t);
-    // the kernel's static shared memory (below 20 KB) counts towards the 48 KB that need no asking
-    if (set_smem<paged_evict_kernel>(smem + 20 * 1024) != LA_OK) return LA_ERR_CUDA;
-    const la_status s1 = launch_pdl_cluster(paged_evict_kernel, (int)(units * cs), kEvictThreads, (int)smem, cs, st, p);
+    const la_status s1 = cs == 1 ? paged_evict_run<4, 4, false>(p, (int)units, 1, st)
+                                 : paged_evict_run<16, 2, true>(p, (int)(units * cs), cs, st);
     if (s1 != LA_OK || !p.newlen) return s1;
     return launch_pdl(paged_evict_lens_kernel, (B + 255) / 256, 256, 0, st, p);
 }

@@ -1184,7 +1184,7 @@ struct PagedEvictParams {
     int keys;              // keys that fit the block's shared memory
 };
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 256;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictMaxKeys = 12288;
@@ -1199,34 +1199,69 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Copies the moved rows of this block's share of the list, eight lanes to a
-// row pair, four pieces in flight per lane.
-template <typename V>
+// Copies the moved rows of this block's share of the list.  A warp takes up to
+// 32 moves, one lane looks up each of them, and then a power of two of lanes
+// copies each row pair, U pairs in flight.
+template <typename V, int U>
 __device__ __forceinline__ void evict_rows(const PagedEvictParams &p, int b, int h, const int *holes,
                                            const int *movers, int m, int rank, int blocks)
 {
-    constexpr int G = 8;
+    constexpr uint32_t ALL = 0xffffffffu;
     const PagedCache &c = p.c;
     const int pk = c.dqk * p.elem / (int)sizeof(V), pv = c.dv * p.elem / (int)sizeof(V), np = pk + pv;
-    const int lane = threadIdx.x % G, step = blocks * (kEvictThreads / G);
+    const int lane = threadIdx.x & 31, warps = blocks * kEvictWarps, wid = rank * kEvictWarps + (threadIdx.x >> 5);
+    int per_row = 1;
+    while (per_row < np && per_row < 32) per_row <<= 1;
+    const int groups = 32 / per_row, sub = lane / per_row, piece0 = lane & (per_row - 1);
+    const int share = min(32, (m + warps - 1) / warps);
     V *kp = (V *)c.kp, *vp = (V *)c.vp;
-    for (int i = rank * (kEvictThreads / G) + threadIdx.x / G; i < m; i += step) {
-        const size_t to = paged_row(c, b, h, holes[i]), from = paged_row(c, b, h, movers[i]);
-        for (int q = lane; q < np; q += 4 * G) {
-            V x[4];
+    for (int i0 = wid * share; i0 < m; i0 += warps * share) {
+        const int cnt = min(share, m - i0);
+        int to = 0, from = 0;
+        if (lane < cnt) {
+            to = paged_row(c, b, h, holes[i0 + lane]);
+            from = paged_row(c, b, h, movers[i0 + lane]);
+        }
+        for (int i = 0; i < cnt; i += U * groups) {
+            int rt[U], rf[U];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = q + j * G;
-                if (at < np) x[j] = at < pk ? kp[from * pk + at] : vp[from * pv + at - pk];
+            for (int u = 0; u < U; ++u) {
+                const int j = i + u * groups + sub;
+                rt[u] = __shfl_sync(ALL, to, j & 31);
+                rf[u] = __shfl_sync(ALL, from, j & 31);
+                if (j >= cnt) rt[u] = -1;
             }
+            for (int q = piece0; q < np; q += per_row) {
+                V x[U];
+                const bool isk = q < pk;
+                V *base = isk ? kp + q : vp + (q - pk);
+                const size_t stride = isk ? pk : pv;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = q + j * G;
-                if (at < pk) kp[to * pk + at] = x[j];
-                else if (at < np) vp[to * pv + at - pk] = x[j];
+                for (int u = 0; u < U; ++u)
+                    if (rt[u] >= 0) x[u] = base[rf[u] * stride];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (rt[u] >= 0) base[rt[u] * stride] = x[u];
             }
         }
     }
+}
+
+// The sum of a warp's value over the warps before this one, and over all.
+// `part` (kEvictWarps words) must not be in use: two buffers in turn.
+__device__ __forceinline__ int warps_before(int x, int *part, int &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) part[warp] = x;
+    __syncthreads();
+    int s = lane < kEvictWarps ? part[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < kEvictWarps; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+    }
+    total = __shfl_sync(0xffffffffu, s, kEvictWarps - 1);
+    return __shfl_sync(0xffffffffu, s, warp) - x;
 }
 
 // One cluster of blocks per (b, h), each block with a slice of the slots.  The
@@ -1237,16 +1272,23 @@ __device__ __forceinline__ void evict_rows(const PagedEvictParams &p, int b, int
 // the ties, list the dropped slots below the budget and the kept ones above it,
 // and move rows, weights and positions along the two lists.  Sources lie at or
 // above the budget and destinations below it, so moves need no order.
-__global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(const PagedEvictParams p)
+template <int U, int BLOCKS, bool CLUSTER>
+__global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(const PagedEvictParams p)
 {
     extern __shared__ __align__(16) int evict_smem[];
-    __shared__ int hist[2][kEvictBins], part[kEvictWarps], pick[3];
-    __shared__ int xch[4];   // read by the cluster's other blocks
+    __shared__ __align__(16) int hist[2][kEvictBins];
+    __shared__ int part[2][kEvictWarps], pick[3];
+    __shared__ int xch[5];   // read by the cluster's other blocks
     namespace cg = cooperative_groups;
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
-    cg::cluster_group cl = cg::this_cluster();
-    const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    // a cluster of up to kEvictMaxCluster blocks, or one block alone
+    const int CS = CLUSTER ? (int)cg::this_cluster().num_blocks() : 1;
+    const int rank = CLUSTER ? (int)cg::this_cluster().block_rank() : 0;
+    auto sync_all = [&]() {
+        if constexpr (CLUSTER) cg::this_cluster().sync();
+        else __syncthreads();
+    };
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const size_t bh = blockIdx.x / CS;
@@ -1288,45 +1330,90 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(const PagedE
         return late ? 0xffffffffu : weight_key(w[t]);
     };
     auto key_of = [&](int t) { return cached ? keys[t - s0] : make_key(t); };
-    // the sum over the cluster's blocks of a value held by thread 0 of each, in `slot`
-    // of xch; also the sum over the blocks before this one.  One barrier each.
-    auto exchange = [&](int slot, int value, int &before) {
-        if (tid == 0) xch[slot] = value;
-        cl.sync();
-        int total = 0;
+    // the sum over the cluster's blocks of their xch[slot], written before a cluster
+    // barrier; also the sum over the blocks before this one
+    auto gather = [&](int slot, int &before) {
         before = 0;
-        for (int i = 0; i < CS; ++i) {
-            const int x = *cl.map_shared_rank(&xch[slot], i);
-            if (i < rank) before += x;
-            total += x;
+        if constexpr (!CLUSTER) {
+            return xch[slot];
+        } else {
+            int x[kEvictMaxCluster], all = 0;
+#pragma unroll
+            for (int i = 0; i < kEvictMaxCluster; ++i) x[i] = i < CS ? *cg::this_cluster().map_shared_rank(&xch[slot], i) : 0;
+#pragma unroll
+            for (int i = 0; i < kEvictMaxCluster; ++i) {
+                if (i < rank) before += x[i];
+                all += x[i];
+            }
+            return all;
         }
-        return total;
     };
 
-    // keys, the number of recent tokens, and the table's entries
-    for (int i = tid; i < 2 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+    // the table's entries; a bad one leaves the sequence as it was
+    for (int i = tid; i < 2 * kEvictBins / 4; i += kEvictThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
     bool bad = false;
     const int used = (n - 1) / c.page + 1;
+#pragma unroll 4
     for (int i = rank * kEvictThreads + tid; i < used; i += CS * kEvictThreads)
-        if ((unsigned)c.table[(size_t)b * c.max_pages + i] >= (unsigned)c.num_pages) bad = true;
-    int late = 0, none;
-    for (int t = a0 + lane; t < a1; t += 32) {
-        const uint32_t key = make_key(t);
-        if (cached) keys[t - s0] = key;
-        late += key == 0xffffffffu;
+        bad |= (unsigned)c.table[(size_t)b * c.max_pages + i] >= (unsigned)c.num_pages;
+    int bads = __syncthreads_or(bad), none;
+    if constexpr (CLUSTER) {
+        if (tid == 0) xch[0] = bads != 0;
+        sync_all();
+        bads = gather(0, none);
     }
-    bad = __syncthreads_or(bad);
-    int total;
-    (void)block_scan<kEvictThreads>(late, part, total);
-    // (a bad table in bit 30: there are fewer than 2^30 recent tokens, or it does not matter which)
-    late = exchange(0, bad ? 1 << 30 : min(total, 1 << 26), none);
-    if (late >= 1 << 30) {
+    if (bads) {
         if (rank == 0 && tid == 0) report(kStatusCheck);
         if (first && p.newlen) len_to[b] = n;
-        cl.sync();   // no block leaves while another reads its xch
+        sync_all();   // no block leaves while another reads its xch
         return;
     }
-    if (late > budget) {
+
+    // f(t0, key, in) for this warp's slots, 32 at a time from t0 on (slot t0 + lane,
+    // `in` if it exists), their keys loaded four times 32 at once
+    auto sweep = [&](auto f) {
+        for (int t = a0; t < a1; t += 128) {
+            uint32_t key[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) key[j] = t + 32 * j + lane < a1 ? key_of(t + 32 * j + lane) : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + 32 * j < a1) f(t + 32 * j, key[j], t + 32 * j + lane < a1);
+        }
+    };
+    // the keys, the number of recent tokens, and the entries of slots that may
+    // stay (those of dropped ones are written again below)
+    int late = 0;
+    for (int t = a0 + lane; t < a1; t += 128) {
+        float x[4];
+        int y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = 0.f;
+            y[j] = 0;
+            if (t + 32 * j < a1) {
+                x[j] = w[t + 32 * j];
+                if (ps) y[j] = ps[t + 32 * j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = t + 32 * j;
+            if (at >= a1) break;
+            const bool l = p.recent && y[j] >= last - p.recent;
+            late += l;
+            if (cached) keys[at - s0] = l ? 0xffffffffu : weight_key(x[j]);
+            if (at < budget) {
+                if (wo != w) wo[at] = x[j];
+                if (po != ps) po[at] = y[j];
+            }
+        }
+    }
+    int total;
+    (void)warps_before(__reduce_add_sync(0xffffffffu, late), part[0], total);
+    if (tid == 0) xch[1] = total;
+    sync_all();
+    if (gather(1, none) > budget) {
         crowded = true;
         if (cached)
             for (int t = a0 + lane; t < a1; t += 32) keys[t - s0] = make_key(t);
@@ -1343,31 +1430,61 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(const PagedE
             for (int i = tid; i < kEvictBins; i += kEvictThreads) hs[i] = 0;
             __syncthreads();
         }
-        for (int t = a0 + lane; t < a1; t += 32) {
-            const uint32_t key = key_of(t);
-            if ((key & known) == thr) atomicAdd(&hs[key >> shift & ((1u << bits) - 1)], 1);
+        sweep([&](int, uint32_t key, bool in) {
+            if (in && (key & known) == thr) atomicAdd(&hs[key >> shift & ((1u << bits) - 1)], 1);
+        });
+        sync_all();
+        // thread i owns BP bins, larger keys first
+        constexpr int BP = kEvictBins / kEvictThreads;
+        const int bin = kEvictBins - BP * (tid + 1);
+        int cnt[BP], mine = 0;
+#pragma unroll
+        for (int j = 0; j < BP; ++j) cnt[j] = 0;
+        constexpr int MAXB = CLUSTER ? kEvictMaxCluster : 1;
+#pragma unroll
+        for (int i0 = 0; i0 < MAXB; i0 += 4) {   // four blocks' bins on their way at once
+            int4 x[4][BP / 4];
+#pragma unroll
+            for (int i = 0; i < 4 && i0 + i < MAXB; ++i) {
+                const int *from = hs;
+                if constexpr (CLUSTER) from = cg::this_cluster().map_shared_rank(hs, i0 + i < CS ? i0 + i : 0);
+#pragma unroll
+                for (int j = 0; j < BP / 4; ++j)
+                    x[i][j] = i0 + i < CS ? reinterpret_cast<const int4 *>(from + bin)[j] : make_int4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4 && i0 + i < MAXB; ++i)
+#pragma unroll
+                for (int j = 0; j < BP / 4; ++j) {
+                    cnt[4 * j] += x[i][j].x;
+                    cnt[4 * j + 1] += x[i][j].y;
+                    cnt[4 * j + 2] += x[i][j].z;
+                    cnt[4 * j + 3] += x[i][j].w;
+                }
         }
-        cl.sync();
-        // thread i owns the four bins from 4 (511 - i) on: larger keys first
-        int4 sum = make_int4(0, 0, 0, 0);
-        const int bin = kEvictBins - 4 - 4 * tid;
-        for (int i = 0; i < CS; ++i) {
-            const int4 x = *reinterpret_cast<const int4 *>(cl.map_shared_rank(hs, i) + bin);
-            sum.x += x.x;
-            sum.y += x.y;
-            sum.z += x.z;
-            sum.w += x.w;
+#pragma unroll
+        for (int j = 0; j < BP; ++j) mine += cnt[j];
+        int scan = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, scan, off);
+            if (lane >= off) scan += o;
         }
-        const int mine = sum.x + sum.y + sum.z + sum.w;
-        int left = need - block_scan<kEvictThreads>(mine, part, total);
+        int left = need - (scan - mine) - warps_before(__shfl_sync(0xffffffffu, scan, 31), part[pass & 1 ? 0 : 1], total);
         if (left > 0 && left <= mine) {   // one thread: the bins add up to at least `need`
-            int at = bin + 3, size = sum.w;
-            if (left > size) left -= size, at = bin + 2, size = sum.z;
-            if (at == bin + 2 && left > size) left -= size, at = bin + 1, size = sum.y;
-            if (at == bin + 1 && left > size) left -= size, at = bin, size = sum.x;
-            pick[0] = at;
-            pick[1] = left;
-            pick[2] = size;
+            bool found = false;
+#pragma unroll
+            for (int j = BP - 1; j >= 0; --j) {
+                if (found) continue;
+                if (left <= cnt[j]) {
+                    pick[0] = bin + j;
+                    pick[1] = left;
+                    pick[2] = cnt[j];
+                    found = true;
+                } else {
+                    left -= cnt[j];
+                }
+            }
         }
         __syncthreads();
         thr |= (uint32_t)pick[0] << shift;
@@ -1380,17 +1497,17 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(const PagedE
     int rank0 = 0;   // ties before this warp's slots
     if (need < ties) {
         int mine = 0;
-        for (int t = a0; t < a1; t += 32) mine += __popc(__ballot_sync(0xffffffffu, t + lane < a1 && key_of(t + lane) == thr));
-        const int before = block_scan<kEvictThreads>(lane == 0 ? mine : 0, part, total);
+        sweep([&](int, uint32_t key, bool in) { mine += __popc(__ballot_sync(0xffffffffu, in && key == thr)); });
+        const int before = warps_before(mine, part[0], total);
+        if (tid == 0) xch[2] = total;
+        sync_all();
         int blocks_before;
-        (void)exchange(1, total, blocks_before);
-        rank0 = blocks_before + __shfl_sync(0xffffffffu, before, 0);
+        (void)gather(2, blocks_before);
+        rank0 = blocks_before + before;
     }
-    // slots t0 .. t0 + 31 of this warp: which are kept
+    // which of 32 slots are kept
     int seen;
-    auto kept = [&](int t0) {
-        const bool in = t0 + lane < a1;
-        const uint32_t key = in ? key_of(t0 + lane) : 0;
+    auto kept = [&](uint32_t key, bool in) {
         bool eq = in && key == thr;
         if (need < ties) {
             const uint32_t all = __ballot_sync(0xffffffffu, eq);
@@ -1404,43 +1521,41 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(const PagedE
     auto exist = [&](int t0) { return t0 + 32 <= a1 ? 0xffffffffu : (1u << (a1 - t0)) - 1; };
     int nh = 0, nm = 0;
     seen = 0;
-    for (int t = a0; t < a1; t += 32) {
-        const uint32_t k = kept(t), lo = below(t);
+    sweep([&](int t, uint32_t key, bool in) {
+        const uint32_t k = kept(key, in), lo = below(t);
         nh += __popc(~k & lo & exist(t));
         nm += __popc(k & ~lo);
-    }
-    int ih = block_scan<kEvictThreads>(lane == 0 ? nh : 0, part, total), blocks_before;
-    ih = __shfl_sync(0xffffffffu, ih, 0);
-    const int m = exchange(2, total, blocks_before);
+    });
+    int ih = warps_before(nh, part[1], total), blocks_before;
+    if (tid == 0) xch[3] = total;
+    __syncthreads();
+    int im = warps_before(nm, part[0], total);
+    if (tid == 0) xch[4] = total;
+    sync_all();
+    const int m = gather(3, blocks_before);
     ih += blocks_before;
-    int im = block_scan<kEvictThreads>(lane == 0 ? nm : 0, part, total);
-    im = __shfl_sync(0xffffffffu, im, 0);
-    (void)exchange(3, total, blocks_before);
+    (void)gather(4, blocks_before);
     im += blocks_before;
     int *holes = p.holes + bh * p.maxmoves, *movers = p.movers + bh * p.maxmoves;
     seen = 0;
-    for (int t = a0; t < a1; t += 32) {
-        const uint32_t k = kept(t), lo = below(t), hole = ~k & lo & exist(t), mover = k & ~lo;
+    sweep([&](int t, uint32_t key, bool in) {
+        const uint32_t k = kept(key, in), lo = below(t), hole = ~k & lo & exist(t), mover = k & ~lo;
         const uint32_t before = (1u << lane) - 1;
         if (hole >> lane & 1) holes[ih + __popc(hole & before)] = t + lane;
         if (mover >> lane & 1) movers[im + __popc(mover & before)] = t + lane;
-        if (k & lo & (1u << lane)) {
-            if (wo != w) wo[t + lane] = w[t + lane];
-            if (po != ps) po[t + lane] = ps[t + lane];
-        }
         ih += __popc(hole);
         im += __popc(mover);
-    }
-    cl.sync();   // the lists are complete, all keys are read, and no block reads another's memory any more
+    });
+    sync_all();   // the lists are complete, all keys are read, and no block reads another's memory any more
     for (int i = rank * kEvictThreads + tid; i < m; i += CS * kEvictThreads) {
         const int to = holes[i], from = movers[i];
         wo[to] = w[from];
         if (po) po[to] = ps[from];
     }
     if (first) len_to[b] = budget;
-    if (p.width == 16) evict_rows<uint4>(p, b, h, holes, movers, m, rank, CS);
-    else if (p.width == 4) evict_rows<uint32_t>(p, b, h, holes, movers, m, rank, CS);
-    else evict_rows<uint16_t>(p, b, h, holes, movers, m, rank, CS);
+    if (p.width == 16) evict_rows<uint4, U>(p, b, h, holes, movers, m, rank, CS);
+    else if (p.width == 4) evict_rows<uint32_t, U>(p, b, h, holes, movers, m, rank, CS);
+    else evict_rows<uint16_t, U>(p, b, h, holes, movers, m, rank, CS);
 }
 
 // lens in place: no block of the kernel above may still read it when it is written.
