@@ -1186,7 +1186,6 @@ struct PagedEvictParams {
 
 constexpr int kEvictThreads = 256;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictBins = 2048;
 constexpr int kEvictMaxKeys = 12288;
 constexpr int kEvictMaxCluster = 8;
 
@@ -1276,7 +1275,8 @@ template <int U, int BLOCKS, bool CLUSTER>
 __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(const PagedEvictParams p)
 {
     extern __shared__ __align__(16) int evict_smem[];
-    __shared__ __align__(16) int hist[2][kEvictBins];
+    constexpr int BITS = CLUSTER ? 8 : 11, BINS = 1 << BITS;   // digits of the radix select
+    __shared__ __align__(16) int hist[2][BINS];
     __shared__ int part[2][kEvictWarps], pick[3];
     __shared__ int xch[5];   // read by the cluster's other blocks
     namespace cg = cooperative_groups;
@@ -1350,7 +1350,7 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
     };
 
     // the table's entries; a bad one leaves the sequence as it was
-    for (int i = tid; i < 2 * kEvictBins / 4; i += kEvictThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
+    for (int i = tid; i < 2 * BINS / 4; i += kEvictThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
     bool bad = false;
     const int used = (n - 1) / c.page + 1;
 #pragma unroll 4
@@ -1420,14 +1420,17 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
         __syncthreads();
     }
 
-    // the radix select, from the top
+    // the radix select, from the top; it ends early when a whole bin stays.  Kept
+    // are the keys whose `known` bits are above thr, and `need` of the `ties`
+    // slots where they are thr.
     uint32_t thr = 0, known = 0;
     int need = budget, ties = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int pass = 0, top = 32; top > 0 && need != ties; ++pass) {
+        const int bits = top < BITS ? top : BITS, shift = top - bits;
+        top = shift;
         int *hs = hist[pass & 1];
-        if (pass == 2) {   // (the other blocks have read it: they have passed the barrier of pass 1)
-            for (int i = tid; i < kEvictBins; i += kEvictThreads) hs[i] = 0;
+        if (pass >= 2) {   // (the other blocks have read it: they have passed the barrier of the last pass)
+            for (int i = tid; i < BINS; i += kEvictThreads) hs[i] = 0;
             __syncthreads();
         }
         sweep([&](int, uint32_t key, bool in) {
@@ -1435,32 +1438,21 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
         });
         sync_all();
         // thread i owns BP bins, larger keys first
-        constexpr int BP = kEvictBins / kEvictThreads;
-        const int bin = kEvictBins - BP * (tid + 1);
+        constexpr int BP = BINS / kEvictThreads;
+        const int bin = BINS - BP * (tid + 1);
         int cnt[BP], mine = 0;
+        if constexpr (CLUSTER) {
+            static_assert(BP == 1, "one bin per thread");
+            int x[kEvictMaxCluster];
 #pragma unroll
-        for (int j = 0; j < BP; ++j) cnt[j] = 0;
-        constexpr int MAXB = CLUSTER ? kEvictMaxCluster : 1;
+            for (int i = 0; i < kEvictMaxCluster; ++i)
+                x[i] = i < CS ? cg::this_cluster().map_shared_rank(hs, i)[bin] : 0;
+            cnt[0] = 0;
 #pragma unroll
-        for (int i0 = 0; i0 < MAXB; i0 += 4) {   // four blocks' bins on their way at once
-            int4 x[4][BP / 4];
+            for (int i = 0; i < kEvictMaxCluster; ++i) cnt[0] += x[i];
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4 && i0 + i < MAXB; ++i) {
-                const int *from = hs;
-                if constexpr (CLUSTER) from = cg::this_cluster().map_shared_rank(hs, i0 + i < CS ? i0 + i : 0);
-#pragma unroll
-                for (int j = 0; j < BP / 4; ++j)
-                    x[i][j] = i0 + i < CS ? reinterpret_cast<const int4 *>(from + bin)[j] : make_int4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4 && i0 + i < MAXB; ++i)
-#pragma unroll
-                for (int j = 0; j < BP / 4; ++j) {
-                    cnt[4 * j] += x[i][j].x;
-                    cnt[4 * j + 1] += x[i][j].y;
-                    cnt[4 * j + 2] += x[i][j].z;
-                    cnt[4 * j + 3] += x[i][j].w;
-                }
+            for (int j = 0; j < BP; j += 4) *reinterpret_cast<int4 *>(cnt + j) = *reinterpret_cast<const int4 *>(hs + bin + j);
         }
 #pragma unroll
         for (int j = 0; j < BP; ++j) mine += cnt[j];
@@ -1493,11 +1485,12 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
         ties = pick[2];
     }
 
-    // `need` of the `ties` slots with key == thr stay, the lowest ones
+    // of the ties, the lowest slots stay
     int rank0 = 0;   // ties before this warp's slots
+    __syncthreads();   // part[0] may have been read last in the select
     if (need < ties) {
         int mine = 0;
-        sweep([&](int, uint32_t key, bool in) { mine += __popc(__ballot_sync(0xffffffffu, in && key == thr)); });
+        sweep([&](int, uint32_t key, bool in) { mine += __popc(__ballot_sync(0xffffffffu, in && (key & known) == thr)); });
         const int before = warps_before(mine, part[0], total);
         if (tid == 0) xch[2] = total;
         sync_all();
@@ -1505,31 +1498,49 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
         (void)gather(2, blocks_before);
         rank0 = blocks_before + before;
     }
-    // which of 32 slots are kept
-    int seen;
-    auto kept = [&](uint32_t key, bool in) {
-        bool eq = in && key == thr;
-        if (need < ties) {
-            const uint32_t all = __ballot_sync(0xffffffffu, eq);
-            eq = eq && rank0 + seen + __popc(all & ((1u << lane) - 1)) < need;
-            seen += __popc(all);
+    // Of the 1024 slots from `base` on, 32 for each lane: those dropped below the
+    // budget, and those kept above it.
+    int seen = 0;   // ties before them
+    auto find = [&](int base, uint32_t &hole, uint32_t &mover) {
+        uint32_t k = 0;
+        for (int i0 = 0; i0 < 32 && base + 32 * i0 < a1; i0 += 4) {
+            uint32_t key[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = base + 32 * (i0 + j) + lane;
+                key[j] = t < a1 ? key_of(t) & known : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = base + 32 * (i0 + j) + lane < a1;
+                bool eq = in && key[j] == thr;
+                if (need < ties) {
+                    const uint32_t all = __ballot_sync(0xffffffffu, eq);
+                    eq = eq && rank0 + seen + __popc(all & ((1u << lane) - 1)) < need;
+                    seen += __popc(all);
+                }
+                const uint32_t keep = __ballot_sync(0xffffffffu, in && (key[j] > thr || eq));
+                if (lane == i0 + j) k = keep;
+            }
         }
-        return __ballot_sync(0xffffffffu, in && (key > thr || eq));
+        const int t0 = base + 32 * lane;
+        const uint32_t exist = t0 + 32 <= a1 ? 0xffffffffu : t0 >= a1 ? 0u : (1u << (a1 - t0)) - 1;
+        const uint32_t below = t0 + 32 <= budget ? 0xffffffffu : t0 >= budget ? 0u : (1u << (budget - t0)) - 1;
+        hole = ~k & exist & below;
+        mover = k & ~below;
     };
-    // among slots t0 .. t0 + 31, those below the budget, and those that exist
-    auto below = [&](int t0) { return t0 + 32 <= budget ? 0xffffffffu : t0 >= budget ? 0u : (1u << (budget - t0)) - 1; };
-    auto exist = [&](int t0) { return t0 + 32 <= a1 ? 0xffffffffu : (1u << (a1 - t0)) - 1; };
+    uint32_t hole = 0, mover = 0;
     int nh = 0, nm = 0;
-    seen = 0;
-    sweep([&](int t, uint32_t key, bool in) {
-        const uint32_t k = kept(key, in), lo = below(t);
-        nh += __popc(~k & lo & exist(t));
-        nm += __popc(k & ~lo);
-    });
-    int ih = warps_before(nh, part[1], total), blocks_before;
+    for (int base = a0; base < a1; base += 1024) {
+        find(base, hole, mover);
+        nh += __popc(hole);
+        nm += __popc(mover);
+    }
+    const bool one = a1 - a0 <= 1024;   // (then the masks are still there below)
+    int ih = warps_before(__reduce_add_sync(0xffffffffu, nh), part[1], total), blocks_before;
     if (tid == 0) xch[3] = total;
     __syncthreads();
-    int im = warps_before(nm, part[0], total);
+    int im = warps_before(__reduce_add_sync(0xffffffffu, nm), part[0], total);
     if (tid == 0) xch[4] = total;
     sync_all();
     const int m = gather(3, blocks_before);
@@ -1538,14 +1549,25 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
     im += blocks_before;
     int *holes = p.holes + bh * p.maxmoves, *movers = p.movers + bh * p.maxmoves;
     seen = 0;
-    sweep([&](int t, uint32_t key, bool in) {
-        const uint32_t k = kept(key, in), lo = below(t), hole = ~k & lo & exist(t), mover = k & ~lo;
-        const uint32_t before = (1u << lane) - 1;
-        if (hole >> lane & 1) holes[ih + __popc(hole & before)] = t + lane;
-        if (mover >> lane & 1) movers[im + __popc(mover & before)] = t + lane;
-        ih += __popc(hole);
-        im += __popc(mover);
-    });
+    for (int base = a0; base < a1; base += 1024) {
+        if (!one) find(base, hole, mover);
+        int sh = __popc(hole), sm = __popc(mover);
+        const int ch = sh, cm = sm;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sh, off), y = __shfl_up_sync(0xffffffffu, sm, off);
+            if (lane >= off) {
+                sh += x;
+                sm += y;
+            }
+        }
+        int *to = holes + ih + sh - ch, t0 = base + 32 * lane;
+        for (uint32_t x = hole; x; x &= x - 1) *to++ = t0 + __ffs(x) - 1;
+        to = movers + im + sm - cm;
+        for (uint32_t x = mover; x; x &= x - 1) *to++ = t0 + __ffs(x) - 1;
+        ih += __shfl_sync(0xffffffffu, sh, 31);
+        im += __shfl_sync(0xffffffffu, sm, 31);
+    }
     sync_all();   // the lists are complete, all keys are read, and no block reads another's memory any more
     for (int i = rank * kEvictThreads + tid; i < m; i += CS * kEvictThreads) {
         const int to = holes[i], from = movers[i];
