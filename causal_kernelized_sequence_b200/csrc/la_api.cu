@@ -1300,7 +1300,7 @@ size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, 
         paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl) != LA_OK)
         return 0;
     size_t bytes = pl.ml_off() + (size_t)pl.grid * 2 * kPagedRows * (sizeof(float2) + dv * sizeof(float));
-    if (with_weights) bytes += (size_t)B * Hq * (pl.stride + 2) * sizeof(float);
+    if (with_weights) bytes += ((size_t)B * Hq * pl.stride + ((size_t)B * Hq + 3) / 4 * 4) * sizeof(float);
     return bytes;
 }
 
@@ -1353,15 +1353,15 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
     p.part = (float *)(p.ml + (size_t)pl.grid * 2 * kPagedRows);
     float *more = p.part + (size_t)pl.grid * 2 * kPagedRows * dv;
     p.stride = pl.stride;
-    // (an even number of floats ahead of the scores keeps their rows 8-byte aligned)
+    // (a multiple of four floats ahead of the scores keeps their rows 16-byte aligned)
     p.lse2 = weights_in ? more : nullptr;
-    p.scores = weights_in ? more + ((size_t)B * Hq + 1) / 2 * 2 : nullptr;
+    p.scores = weights_in ? more + ((size_t)B * Hq + 3) / 4 * 4 : nullptr;
     cudaStream_t st = (cudaStream_t)stream;
     const la_status s1 = pl.mma ? paged_mma(p, pl, st)
                          : dtype == LA_F32 ? paged_simt<float>(p, pl, st) : paged_simt<__nv_bfloat16>(p, pl, st);
     if (s1 != LA_OK) return s1;
-    if (dtype == LA_F32) return launch_pdl(paged_join_kernel<float>, pl.grid, kPagedThreads, 0, st, p);
-    return launch_pdl(paged_join_kernel<__nv_bfloat16>, pl.grid, kPagedThreads, 0, st, p);
+    if (dtype == LA_F32) return launch_pdl(paged_join_kernel<float>, pl.grid, kPagedJoinThreads, 0, st, p);
+    return launch_pdl(paged_join_kernel<__nv_bfloat16>, pl.grid, kPagedJoinThreads, 0, st, p);
 }
 
 // Most slots that can move in one (b, h): as many as lie below the budget, or above it.

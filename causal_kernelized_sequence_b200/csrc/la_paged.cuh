@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 
 constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
+constexpr int kPagedJoinThreads = 256;
 constexpr int kPagedRows = 16;       // query heads of a unit
 constexpr int kPagedMaxGroup = 128;  // query heads per key/value head
 
@@ -1053,9 +1054,9 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
     const size_t hq0 = (size_t)s.b * p.Hq + h * p.g + sub * p.gs;
     const int E = rows * dv, per = (E + K - 1) / K, e0 = (blockIdx.x - g0) * per, e1 = min(E, e0 + per);
     int KL = 1;
-    while (KL < K && KL < 32 && per * KL * 2 <= kPagedThreads) KL <<= 1;
+    while (KL < K && KL < 32 && per * KL * 2 <= kPagedJoinThreads) KL <<= 1;
     const int mine = threadIdx.x & (KL - 1);
-    for (int base = e0; base < e1; base += kPagedThreads / KL) {   // the same count for every thread
+    for (int base = e0; base < e1; base += kPagedJoinThreads / KL) {   // the same count for every thread
         const int e = base + threadIdx.x / KL;
         const bool on = e < e1;
         const int row = on ? e / dv : 0, col = on ? e - row * dv : 0;
@@ -1104,7 +1105,7 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedDecodeParams p)
+__global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const PagedDecodeParams p)
 {
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
@@ -1129,7 +1130,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedDe
         if (w.sub == 0 && w.n > 0) {
             const size_t hq0 = w.hq(p), bh = w.bh(p);
             __syncthreads();
-            for (int j = tid; j < p.g; j += kPagedThreads) {
+            for (int j = tid; j < p.g; j += kPagedJoinThreads) {
                 const int sub = j / p.gs;
                 const long long first = at - w.tile + (long long)sub * w.nt;   // of this head's unit
                 const int g0 = (int)(first / rec.chunk), g1 = (int)((first + w.nt - 1) / rec.chunk);
@@ -1148,13 +1149,31 @@ __global__ void __launch_bounds__(kPagedThreads) paged_join_kernel(const PagedDe
                 }
             }
             __syncthreads();
+            // four neighbouring slots per thread: a tile's scores start on 16 bytes
             const int end = min((long long)w.n, (long long)(w.tile + here) << p.tile);
-            for (int t = (w.tile << p.tile) + tid; t < end; t += kPagedThreads) {
-                float sum = 0.f;
-                for (int j = 0; j < p.g; ++j)
-                    if (lse2[j] != -INFINITY) sum += ex2(p.scores[(hq0 + j) * p.stride + t] - lse2[j]);
-                const size_t to = bh * c.cap() + t;
-                p.w_out[to] = (p.k && t == w.n - 1 ? 0.f : p.w_in[to]) + sum;
+            const float *wi = p.w_in + bh * c.cap();
+            float *wo = p.w_out + bh * c.cap();
+            for (int t = (w.tile << p.tile) + 4 * tid; t < end; t += 4 * kPagedJoinThreads) {
+                float sum[4], old[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    old[e] = t + e < end && !(p.k && t + e == w.n - 1) ? wi[t + e] : 0.f;
+                    sum[e] = 0.f;
+                }
+#pragma unroll 4
+                for (int j = 0; j < p.g; ++j) {
+                    const float4 s = *reinterpret_cast<const float4 *>(p.scores + (hq0 + j) * p.stride + t);
+                    const float L = lse2[j];
+                    if (L != -INFINITY) {
+                        sum[0] += ex2(s.x - L);
+                        sum[1] += ex2(s.y - L);
+                        sum[2] += ex2(s.z - L);
+                        sum[3] += ex2(s.w - L);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t + e < end) wo[t + e] = old[e] + sum[e];
             }
         }
         left -= here;
