@@ -704,61 +704,75 @@ static la_status check_paged_ptrs(const void *kp, const void *vp, const int32_t 
     return LA_OK;
 }
 
-// How a decode step is cut up: units of at most 16 query heads, one range of
-// tiles per block.
+// How a decode step is cut up: units of at most 16 query heads, and one range of
+// tiles per block, or one unit per block.
 struct PagedPlan {
-    bool mma;
+    bool mma, tma, aligned;
     int nsub, gs, grid, tile;
     int64_t stride;   // slots per row of kept scores: whole tiles
     size_t ml_off() const { return ((size_t)grid * sizeof(PagedRecord) + 15) / 16 * 16; }
 };
 
-static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages, int dtype,
-                            PagedPlan *pl)
+static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages, bool weights,
+                            int dtype, PagedPlan *pl)
 {
     const int g = Hq / Hkv;
     if (g > kPagedMaxGroup) return LA_ERR_UNSUPPORTED;
-    pl->mma = dtype == LA_BF16 && dqk % 8 == 0 && dv % 8 == 0;
+    pl->tma = rows16(dqk, dtype) && rows16(dv, dtype);
+    pl->mma = dtype == LA_BF16 && pl->tma;
     pl->nsub = (g + kPagedRows - 1) / kPagedRows;
     pl->gs = (g + pl->nsub - 1) / pl->nsub;
     // as many blocks as an SM holds (BLOCKS of the kernels' configurations)
     const bool narrow = dqk <= 64 && dv <= 64;
-    pl->grid = kNumSms * (pl->mma ? (narrow ? 3 : 2) : (narrow ? 2 : 1));
+    pl->grid = kNumSms * (narrow && (pl->mma || pl->gs <= 4) ? 3 : 2);
     pl->tile = pl->mma ? 7 : 6;
-    const int64_t tiles = (((int64_t)max_pages * page_size - 1) >> pl->tile) + 1;
+    const int64_t tiles = (((int64_t)max_pages * page_size - 1) >> pl->tile) + 1, units = (int64_t)B * Hkv * pl->nsub;
     pl->stride = tiles << pl->tile;
     // a range's length and a unit's tiles are 32-bit
-    if ((int64_t)B * Hkv * pl->nsub >= (int64_t)1 << 31 || (double)tiles * B * Hkv * pl->nsub / pl->grid >= 2e9)
-        return LA_ERR_INVALID_ARG;
+    if (units >= (int64_t)1 << 31 || (double)tiles * units / pl->grid >= 2e9) return LA_ERR_INVALID_ARG;
+    // Few and short sequences: a block walks through a whole unit in less time
+    // than the join's launch takes, and needs no scan over the lengths.
+    pl->aligned = !weights && units <= pl->grid && tiles <= 4;
+    if (pl->aligned) pl->grid = (int)units;
     return LA_OK;
 }
 
 // The pool as rows of d elements, boxes of `rows` x 128 bytes in SW128.
-static bool make_pool_map(CUtensorMap *m, const void *base, const PagedCache &c, int d, int rows)
+static bool make_pool_map(CUtensorMap *m, const void *base, const PagedCache &c, int d, int rows, int dtype)
 {
     auto fn = encode_fn();
     if (!fn) return false;
+    const int el = (int)elem_size(dtype);
     cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)c.num_pages * c.Hkv * c.page};
-    cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)d * el};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / el), (cuuint32_t)rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, dtype == LA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// Maps of the two pools.  A warp's slots of a tile start at a multiple of
+// `slots`, so a box of a power of two of slots that divides the page size never
+// leaves its page.
+static la_status paged_maps(PagedDecodeParams *p, int slots, int dtype, CUtensorMap *tk, CUtensorMap *tv)
+{
+    p->box_rows = slots;
+    while (p->c.page % p->box_rows) p->box_rows /= 2;
+    const int rows = p->box_rows < 4 ? 1 : p->box_rows;
+    return make_pool_map(tk, p->c.kp, p->c, p->c.dqk, rows, dtype) &&
+                   make_pool_map(tv, p->c.vp, p->c, p->c.dv, rows, dtype)
+               ? LA_OK
+               : LA_ERR_CUDA;
 }
 
 template <int DQ, int DV, bool HI>
 static la_status paged_mma_run(PagedDecodeParams p, const PagedPlan &pl, cudaStream_t st)
 {
     using Cfg = PagedMma<DQ, DV, HI>;
-    // a chunk of 32 slots starts at a multiple of 32, so a box of a power of two
-    // of slots that divides the page size never leaves its page
-    p.box_rows = 32;
-    while (p.c.page % p.box_rows) p.box_rows /= 2;
-    const int rows = p.box_rows < 4 ? 1 : p.box_rows;
     CUtensorMap tk, tv;
-    if (!make_pool_map(&tk, p.c.kp, p.c, p.c.dqk, rows) || !make_pool_map(&tv, p.c.vp, p.c, p.c.dv, rows))
-        return LA_ERR_CUDA;
+    if (paged_maps(&p, 32, LA_BF16, &tk, &tv) != LA_OK) return LA_ERR_CUDA;
     if (set_smem<paged_decode_mma_kernel<DQ, DV, HI>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
     return launch_pdl(paged_decode_mma_kernel<DQ, DV, HI>, pl.grid, kPagedThreads, Cfg::SMEM, st, tk, tv, p);
 }
@@ -774,23 +788,26 @@ static la_status paged_mma(const PagedDecodeParams &p, const PagedPlan &pl, cuda
     return hi ? paged_mma_run<128, 128, true>(p, pl, st) : paged_mma_run<128, 128, false>(p, pl, st);
 }
 
-template <typename T, int D, int GM>
-static la_status paged_simt_run(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+template <typename T, int D, int GM, bool TMA>
+static la_status paged_simt_run(PagedDecodeParams p, const PagedPlan &pl, cudaStream_t st)
 {
-    using Cfg = PagedSimt<T, D, GM>;
-    if (set_smem<paged_decode_simt_kernel<T, D, GM>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
-    return launch_pdl(paged_decode_simt_kernel<T, D, GM>, pl.grid, kPagedThreads, Cfg::SMEM, st, p);
+    using Cfg = PagedSimt<T, D, GM, TMA>;
+    CUtensorMap tk = {}, tv = {};
+    p.box_rows = 0;
+    if (TMA && paged_maps(&p, 16, LA_F32, &tk, &tv) != LA_OK) return LA_ERR_CUDA;
+    if (set_smem<paged_decode_simt_kernel<T, D, GM, TMA>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
+    return launch_pdl(paged_decode_simt_kernel<T, D, GM, TMA>, pl.grid, kPagedThreads, Cfg::SMEM, st, tk, tv, p);
 }
 
-template <typename T>
+template <typename T, bool TMA>
 static la_status paged_simt(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
 {
     if (p.c.dqk <= 64 && p.c.dv <= 64) {
-        if (pl.gs == 1) return paged_simt_run<T, 64, 1>(p, pl, st);
-        return pl.gs <= 4 ? paged_simt_run<T, 64, 4>(p, pl, st) : paged_simt_run<T, 64, 16>(p, pl, st);
+        if (pl.gs == 1) return paged_simt_run<T, 64, 1, TMA>(p, pl, st);
+        return pl.gs <= 4 ? paged_simt_run<T, 64, 4, TMA>(p, pl, st) : paged_simt_run<T, 64, 16, TMA>(p, pl, st);
     }
-    if (pl.gs == 1) return paged_simt_run<T, 128, 1>(p, pl, st);
-    return pl.gs <= 4 ? paged_simt_run<T, 128, 4>(p, pl, st) : paged_simt_run<T, 128, 16>(p, pl, st);
+    if (pl.gs == 1) return paged_simt_run<T, 128, 1, TMA>(p, pl, st);
+    return pl.gs <= 4 ? paged_simt_run<T, 128, 4, TMA>(p, pl, st) : paged_simt_run<T, 128, 16, TMA>(p, pl, st);
 }
 
 // The eviction with U row pairs in flight per warp, BLOCKS blocks on an SM.
@@ -1297,8 +1314,9 @@ size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, 
 {
     PagedPlan pl;
     if (check_paged(B, Hq, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK ||
-        paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl) != LA_OK)
+        paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, with_weights != 0, dtype, &pl) != LA_OK)
         return 0;
+    if (pl.aligned) return 0;
     size_t bytes = pl.ml_off() + (size_t)pl.grid * 2 * kPagedRows * (sizeof(float2) + dv * sizeof(float));
     if (with_weights) bytes += ((size_t)B * Hq * pl.stride + ((size_t)B * Hq + 3) / 4 * 4) * sizeof(float);
     return bytes;
@@ -1323,11 +1341,11 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
     if (!same_or_apart(weights_in, weights_out, (size_t)B * Hkv * max_pages * page_size * sizeof(float)))
         return LA_ERR_INVALID_ARG;
     PagedPlan pl;
-    const la_status ps = paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl);
+    const la_status ps = paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, weights_in != nullptr, dtype, &pl);
     if (ps != LA_OK) return ps;
     const size_t need = la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page_size, max_pages,
                                                         weights_in != nullptr, dtype);
-    if (workspace_bytes < need || !workspace || !aligned(workspace, 16)) return LA_ERR_INVALID_ARG;
+    if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return LA_ERR_INVALID_ARG;
     if (check_on_current_device(k_pages) != LA_OK) return LA_ERR_INVALID_ARG;
     PagedDecodeParams p;
     p.c = make_paged(k_pages, v_pages, block_table, lens, B, Hkv, dqk, dv, num_pages, page_size, max_pages);
@@ -1345,8 +1363,8 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
     p.nsub = pl.nsub;
     p.gs = pl.gs;
     p.tile = pl.tile;
+    p.aligned = pl.aligned;
     p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)dqk));
-    p.vec = rows16(dqk, dtype) && rows16(dv, dtype);
     uint8_t *ws = (uint8_t *)workspace;
     p.rec = (PagedRecord *)ws;
     p.ml = (float2 *)(ws + pl.ml_off());
@@ -1357,9 +1375,11 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
     p.lse2 = weights_in ? more : nullptr;
     p.scores = weights_in ? more + ((size_t)B * Hq + 3) / 4 * 4 : nullptr;
     cudaStream_t st = (cudaStream_t)stream;
-    const la_status s1 = pl.mma ? paged_mma(p, pl, st)
-                         : dtype == LA_F32 ? paged_simt<float>(p, pl, st) : paged_simt<__nv_bfloat16>(p, pl, st);
-    if (s1 != LA_OK) return s1;
+    const la_status s1 = pl.mma             ? paged_mma(p, pl, st)
+                         : pl.tma           ? paged_simt<float, true>(p, pl, st)
+                         : dtype == LA_F32  ? paged_simt<float, false>(p, pl, st)
+                                            : paged_simt<__nv_bfloat16, false>(p, pl, st);
+    if (s1 != LA_OK || pl.aligned) return s1;
     if (dtype == LA_F32) return launch_pdl(paged_join_kernel<float>, pl.grid, kPagedJoinThreads, 0, st, p);
     return launch_pdl(paged_join_kernel<__nv_bfloat16>, pl.grid, kPagedJoinThreads, 0, st, p);
 }
@@ -1436,21 +1456,21 @@ la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_tabl
 int la_paged_kernel_plan(int op, int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
                          int with_weights, int dtype, char *buf, size_t buflen)
 {
-    (void)with_weights;
     if (op < 0 || op > 2 ||
         check_paged(B, op == 1 ? Hq : Hkv, Hkv, dqk, dv, 1, page_size, max_pages, dtype) != LA_OK)
         return -1;
     PagedPlan pl;
-    if (op == 1 && paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, dtype, &pl) != LA_OK) return -1;
+    if (op == 1 && paged_plan(B, Hq, Hkv, dqk, dv, page_size, max_pages, with_weights != 0, dtype, &pl) != LA_OK) return -1;
     const char *nm = op == 0   ? "paged_fill_kernel"
                      : op == 2 ? "paged_evict_kernel,paged_evict_lens_kernel"
+                     : pl.aligned ? (pl.mma ? "paged_decode_mma_kernel" : "paged_decode_simt_kernel")
                      : pl.mma  ? "paged_decode_mma_kernel,paged_join_kernel"
                                : "paged_decode_simt_kernel,paged_join_kernel";
     if (buf && buflen) {
         strncpy(buf, nm, buflen - 1);
         buf[buflen - 1] = 0;
     }
-    return op == 0 ? 1 : 2;
+    return op == 0 || (op == 1 && pl.aligned) ? 1 : 2;
 }
 
 la_status la_feature_map(const void *x, void *phi, int64_t rows, int dqk, int fmap, int dtype,

@@ -147,8 +147,8 @@ struct PagedDecodeParams {
     const int *pos;
     int Hq, g, nsub, gs;     // query heads; per key/value head; units per head; heads per unit
     int tile;                // log2 of the slots per tile
+    bool aligned;            // one unit per block, nothing to join
     float scale_log2;        // log2(e) / sqrt(dqk)
-    bool vec;                // rows start on 16-byte boundaries
     int box_rows;            // slots per TMA box: 32, 16, 8 or 4, or below 4: gathered by fours
     PagedRecord *rec;        // [grid]
     float2 *ml;              // [grid][2][16]: running maximum and sum of the head and tail parts
@@ -159,11 +159,14 @@ struct PagedDecodeParams {
 };
 
 // Slots that sequence b attends to, or -1 if its length or position is bad.
+__device__ __forceinline__ int paged_count(const PagedDecodeParams &p, int len, int pos)
+{
+    const int more = p.k ? 1 : 0;
+    return len < 0 || len > p.c.cap() - more || pos < 0 ? -1 : len + more;
+}
 __device__ __forceinline__ int paged_count(const PagedDecodeParams &p, int b)
 {
-    const int len = p.c.lens[b], more = p.k ? 1 : 0;
-    if (len < 0 || len > p.c.cap() - more || (p.pos && p.pos[b] < 0)) return -1;
-    return len + more;
+    return paged_count(p, p.c.lens[b], p.pos ? p.pos[b] : 0);
 }
 __device__ __forceinline__ int paged_tiles(const PagedDecodeParams &p, int n)
 {
@@ -197,13 +200,21 @@ __device__ __forceinline__ I block_scan(I x, I *part, I &total)
 // A position in the (b, h, sub, tile) order; (h, sub) is a unit, u = h nsub + sub.
 struct PagedWalk {
     int b, h, sub, tile, nt, n;
-    __device__ __forceinline__ void load(const PagedDecodeParams &p)
+    __device__ __forceinline__ int rows(const PagedDecodeParams &p) const { return min(p.gs, p.g - sub * p.gs); }
+    // its first query head, and its key/value head, of all sequences
+    __device__ __forceinline__ size_t hq(const PagedDecodeParams &p) const
     {
-        n = paged_count(p, b);
-        nt = paged_tiles(p, n);
+        return (size_t)b * p.Hq + h * p.g + sub * p.gs;
     }
-    // to the next tile (not past the last sequence)
-    __device__ __forceinline__ void next(const PagedDecodeParams &p)
+    __device__ __forceinline__ size_t bh(const PagedDecodeParams &p) const { return (size_t)b * p.c.Hkv + h; }
+    __device__ __forceinline__ void set(const PagedDecodeParams &p, int count)
+    {
+        n = count;
+        nt = paged_tiles(p, count);
+    }
+    // to the next tile (not past the last sequence); `count` gives a sequence's slots
+    template <typename F>
+    __device__ __forceinline__ void next(const PagedDecodeParams &p, F count)
     {
         if (++tile < nt) return;
         tile = 0;
@@ -212,15 +223,8 @@ struct PagedWalk {
         if (++h < p.c.Hkv) return;
         h = 0;
         ++b;
-        load(p);
+        set(p, count(b));
     }
-    __device__ __forceinline__ int rows(const PagedDecodeParams &p) const { return min(p.gs, p.g - sub * p.gs); }
-    // its first query head, and its key/value head, of all sequences
-    __device__ __forceinline__ size_t hq(const PagedDecodeParams &p) const
-    {
-        return (size_t)b * p.Hq + h * p.g + sub * p.gs;
-    }
-    __device__ __forceinline__ size_t bh(const PagedDecodeParams &p) const { return (size_t)b * p.c.Hkv + h; }
 };
 
 // This block's range: sets the walk to its start and returns its number of
@@ -229,6 +233,16 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
                                            long long *part)
 {
     long long *found = part + kPagedWarps;
+    if (p.aligned) {   // one unit per block
+        const int u = blockIdx.x % (p.c.Hkv * p.nsub);
+        w.b = blockIdx.x / (p.c.Hkv * p.nsub);
+        w.h = u / p.nsub;
+        w.sub = u - w.h * p.nsub;
+        w.tile = 0;
+        w.set(p, paged_count(p, w.b));
+        first = chunk = 0;
+        return w.nt;
+    }
     const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
     const int slab = (B + kPagedThreads - 1) / kPagedThreads, b0 = min(B, tid * slab), b1 = min(B, b0 + slab);
     long long mine = 0, total;
@@ -251,7 +265,7 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
     __syncthreads();
     if (first >= total) return 0;
     w.b = (int)found[0];
-    w.load(p);
+    w.set(p, paged_count(p, w.b));
     const long long off = first - U * found[1];   // below U * nt
     const int u = (int)(off / w.nt);
     w.h = u / p.nsub;
@@ -264,6 +278,7 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
 __device__ __forceinline__ void paged_record(const PagedDecodeParams &p, const PagedWalk &w, int tiles,
                                              long long chunk)
 {
+    if (p.aligned) return;
     PagedRecord &r = p.rec[blockIdx.x];
     r.head.b = r.tail.b = -1;
     r.tiles = tiles;
@@ -273,16 +288,16 @@ __device__ __forceinline__ void paged_record(const PagedDecodeParams &p, const P
     r.tile = w.tile;
 }
 
-// Where one unit's part of a range ends: the four warps' rows r0 .. r0 + 7 lie
-// in obuf [warp][8][DV] and their maxima and sums in mls [warp][16].  Finishes
+// Where one unit's part of a range ends: the four warps' rows r0 .. r0 + OR - 1
+// lie in obuf [warp][OR][DV] and their maxima and sums in mls [warp][16].  Finishes
 // the rows (`whole`) or leaves them to the join as part `slot`.
-template <typename T, int DV>
+template <typename T, int DV, int OR>
 __device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const PagedWalk &w, const float *obuf,
                                             const float2 *mls, int r0, int rows, bool whole, int slot)
 {
     const int tid = threadIdx.x, col = tid % DV;
     const size_t hq0 = w.hq(p);
-    for (int r = tid / DV; r < 8 && r0 + r < rows; r += kPagedThreads / DV) {
+    for (int r = tid / DV; r < OR && r0 + r < rows; r += kPagedThreads / DV) {
         float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll
         for (int i = 0; i < kPagedWarps; ++i) M = fmaxf(M, mls[i * kPagedRows + r0 + r].x);
@@ -292,7 +307,7 @@ __device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const Pa
             const float2 e = mls[i * kPagedRows + r0 + r];
             const float f = exp2f(e.x - base);
             L = fmaf(f, e.y, L);
-            acc = fmaf(f, obuf[(i * 8 + r) * DV + col], acc);
+            acc = fmaf(f, obuf[(i * OR + r) * DV + col], acc);
         }
         if (whole) {
             const bool none = L == 0.f;   // nothing to attend to
@@ -307,19 +322,6 @@ __device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const Pa
             if (col == 0) p.ml[at] = make_float2(M, L);
         }
     }
-}
-
-// The new token of the unit's sequence goes to its slot (once per head).
-template <typename T>
-__device__ __forceinline__ void paged_store_new(const PagedDecodeParams &p, const PagedWalk &w)
-{
-    const PagedCache &c = p.c;
-    const int t = w.n - 1, row = paged_row(c, w.b, w.h, t), tid = threadIdx.x;
-    const size_t bh = w.bh(p);
-    if (row < 0) return;
-    for (int i = tid; i < c.dqk; i += kPagedThreads) ((T *)c.kp)[(size_t)row * c.dqk + i] = ((const T *)p.k)[bh * c.dqk + i];
-    for (int i = tid; i < c.dv; i += kPagedThreads) ((T *)c.vp)[(size_t)row * c.dv + i] = ((const T *)p.v)[bh * c.dv + i];
-    if (p.positions && tid == 0) p.positions[bh * c.cap() + t] = p.pos[w.b];
 }
 
 // The end of a unit's part [t0, w.tile] of a range: whether it is whole, and
@@ -340,27 +342,23 @@ __device__ __forceinline__ int paged_part(const PagedDecodeParams &p, const Page
     return slot;
 }
 
-constexpr int kPagedNone = -1, kPagedNew = -2;   // rows that are not in the pool
-
-// Row of slot t of the walk's unit: kPagedNone past the end or on a bad page,
-// kPagedNew for the new token, which is read from the caller's k, v.  `page` is
-// the table's entry, fetched earlier by paged_entry.
+// The table's entry for slot t of the walk's unit, and the slot's row in the pool
+// with that entry: -1 past the end or on a bad page.
 __device__ __forceinline__ int paged_entry(const PagedDecodeParams &p, const PagedWalk &w, int t)
 {
     if (t >= w.n) return -1;
     return p.c.table[(size_t)w.b * p.c.max_pages + (p.c.shift >= 0 ? t >> p.c.shift : t / p.c.page)];
 }
-__device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const PagedWalk &w, int t, int page)
+__device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const PagedWalk &w, int t, int entry)
 {
     const PagedCache &c = p.c;
-    if (t >= w.n) return kPagedNone;
-    if ((unsigned)page >= (unsigned)c.num_pages) {
+    if (t >= w.n) return -1;
+    if ((unsigned)entry >= (unsigned)c.num_pages) {
         report(kStatusCheck);
-        return kPagedNone;
+        return -1;
     }
-    if (p.k && t == w.n - 1) return kPagedNew;
     const int off = c.shift >= 0 ? t & (c.page - 1) : t % c.page;
-    return (page * c.Hkv + w.h) * c.page + off;
+    return (entry * c.Hkv + w.h) * c.page + off;
 }
 
 // 2^x; results below 2^-126 are 0.
@@ -371,21 +369,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// 16 bytes from global to shared memory, or 16 zero bytes.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
@@ -415,14 +398,248 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
     return bf16x2(lo - __uint_as_float(r << 16), hi - __uint_as_float(r & 0xffff0000u));
 }
 
+// ---- a warp's keys and values, from the pool to shared memory
+//
+// Each warp brings the keys, then the values, of its quarter of the next tiles
+// (SLOTS slots) into its own ring of shared memory, ST loads deep.  A place of
+// the ring holds blocks of 128 bytes per slot, in the 128-byte swizzle: 16-byte
+// piece i of slot t lies at piece i ^ (t mod 8).  By TMA, with one mbarrier per
+// place: slots of a page are neighbouring rows of the pool, so a box of
+// `box_rows` rows (32, 16, 8 or 4, whichever divides the page size) is one copy
+// per block; pages of other sizes gather four rows by index.  Rows that do not
+// start on 16 bytes cannot be copied by TMA: the lanes load their elements.
+// Nothing but the wait for its own copies orders a warp inside a unit.
+//
+// What the consumer has to know of a tile (below) lies beside the ring, so only
+// the loads walk through the sequences; the length of the sequence after the
+// walk's is on its way while the walk is in this one.
+struct __align__(16) PagedTile {
+    uint32_t mask;     // slots attended to
+    uint32_t copies;   // copies that fill them: 0, nothing to wait for
+    int newrow;        // row of the new token if it is among them, else -1
+    int n, b, h, sub, tile;
+};
+
+// Tiles kept beside the ring: with at most four places, the keys of tile i + 2
+// are asked for after tile i has been read, and tile i + 1 is still there.
+constexpr int kPagedAhead = 2;
+
+template <typename T, typename E, int KB, int VB, int SLOTS, int ST, bool TMA>
+struct PagedFeed {
+    static_assert(ST <= 4, "kPagedAhead");
+    static constexpr uint32_t ALL = 0xffffffffu;
+    static constexpr int BLOCK = SLOTS * 128, PLACE = (KB > VB ? KB : VB) * BLOCK;
+    static constexpr int COLS = 128 / sizeof(E);   // elements of a block's row: E in shared memory, T in the pool
+    const PagedDecodeParams &p;
+    const CUtensorMap *tm_k, *tm_v;
+    uint8_t *ring;
+    uint64_t *full;
+    PagedTile *tiles_at;
+    PagedWalk w;                 // the tile whose loads are next
+    int tiles, issued, place_in, place_out, warp, lane, entry, row;
+    int next_len, next_pos;      // of sequence w.b + 1
+    uint32_t copies, pending, phases;
+    bool alive;                  // false once a wait ran out: tiles go by without loads and without slots
+
+    __device__ __forceinline__ PagedFeed(const PagedDecodeParams &p_, const CUtensorMap *k, const CUtensorMap *v,
+                                         uint8_t *ring_, uint64_t *full_, PagedTile *at, const PagedWalk &w_, int tiles_)
+        : p(p_), tm_k(k), tm_v(v), ring(ring_), full(full_), tiles_at(at), w(w_), tiles(tiles_), issued(0), place_in(0),
+          place_out(0), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), row(-1), copies(0), pending(0), phases(0),
+          alive(true)
+    {
+        ahead();
+        entry = paged_entry(p, w, slot());
+    }
+    __device__ __forceinline__ int slot() const
+    {
+        return SLOTS == 32 || lane < SLOTS ? (w.tile * 4 + warp) * SLOTS + lane : INT_MAX;
+    }
+    __device__ __forceinline__ void ahead()
+    {
+        next_len = next_pos = 0;
+        if (w.b + 1 < p.c.B) {
+            next_len = p.c.lens[w.b + 1];
+            if (p.pos) next_pos = p.pos[w.b + 1];
+        }
+    }
+    __device__ __forceinline__ void advance()
+    {
+        const int b = w.b;
+        w.next(p, [&](int) { return paged_count(p, next_len, next_pos); });
+        if (w.b != b) ahead();
+        entry = paged_entry(p, w, slot());
+    }
+    // the next load into the ring, if there is one
+    __device__ __forceinline__ void issue()
+    {
+        using namespace sm100;
+        if (issued >= 2 * tiles) return;
+        const bool isv = issued & 1;
+        const int group = p.box_rows < 4 ? 4 : p.box_rows < SLOTS ? p.box_rows : SLOTS;   // slots per copy
+        if (!isv) {
+            row = alive ? paged_entry_row(p, w, slot(), entry) : -1;
+            const uint32_t mask = __ballot_sync(ALL, row >= 0);
+            const bool fresh = p.k && row >= 0 && slot() == w.n - 1;   // the new token: not in the pool yet
+            const uint32_t newmask = __ballot_sync(ALL, fresh), held = mask & ~newmask;
+            const int newrow = newmask ? __shfl_sync(ALL, row, __ffs(newmask) - 1) : -1;
+            // a box lies in one page: its first slot is held if any is; four gathered
+            // rows are brought in if any is held
+            copies = 0;
+            if (TMA) copies = __ballot_sync(ALL, (lane & (group - 1)) == 0 && (held >> lane & (group == 32 ? ALL : (1u << group) - 1)));
+            else if (fresh) row = -1;
+            if (lane == 0) {
+                int4 *to = reinterpret_cast<int4 *>(tiles_at + (issued >> 1) % kPagedAhead);
+                to[0] = make_int4((int)mask, (int)copies, newrow, w.n);
+                to[1] = make_int4(w.b, w.h, w.sub, w.tile);
+            }
+            if (!TMA) copies = held;
+            if ((issued >> 1) + 1 < tiles) advance();
+        }
+        if (!alive) copies = 0;
+        if (copies) {
+            uint8_t *dst = ring + place_in * PLACE;
+            if constexpr (TMA) {
+                const CUtensorMap *map = isv ? tm_v : tm_k;
+                if (lane == 0) mbar_arrive_expect_tx(full + place_in, __popc(copies) * group * 128 * (isv ? VB : KB));
+                int y1, y2, y3;   // of rows that are not held: row 0 or the new token's, whose places are not used
+                if (p.box_rows < 4) {
+                    y1 = max(__shfl_down_sync(ALL, row, 1), 0);
+                    y2 = max(__shfl_down_sync(ALL, row, 2), 0);
+                    y3 = max(__shfl_down_sync(ALL, row, 3), 0);
+                }
+                __syncwarp();
+                if (copies >> lane & 1) {
+#pragma unroll
+                    for (int j = 0; j < (KB > VB ? KB : VB); ++j) {
+                        if (j >= (isv ? VB : KB)) break;
+                        if (p.box_rows < 4)
+                            tma_gather4(dst + j * BLOCK + lane * 128, map, full + place_in, j * COLS, max(row, 0), y1, y2, y3);
+                        else
+                            tma_load_2d(dst + j * BLOCK + lane * 128, map, full + place_in, j * COLS, row);
+                    }
+                }
+                pending |= 1u << place_in;
+            } else {
+                // eight lanes per slot, four elements at a time
+                const int d = isv ? p.c.dv : p.c.dqk;
+                const T *pool = (const T *)(isv ? p.c.vp : p.c.kp);
+#pragma unroll 1
+                for (int s0 = 0; s0 < SLOTS; s0 += 4) {
+                    const int s = s0 + (lane >> 3), r = __shfl_sync(ALL, row, s);
+#pragma unroll 1
+                    for (int j = 0; j * 32 < d; ++j) {
+                        const int col = j * 32 + (lane & 7) * 4;
+                        float x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = r >= 0 && col + e < d ? ld(pool + (size_t)r * d + col + e) : 0.f;
+                        *reinterpret_cast<float4 *>(dst + j * BLOCK + s * 128 + (((lane ^ s) & 7) << 4)) =
+                            make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        ++issued;
+        if (++place_in == ST) place_in = 0;
+    }
+    // the next place of the ring, once its copies have landed
+    __device__ __forceinline__ uint8_t *take(bool copied)
+    {
+        if (TMA && copied && alive) {
+            alive = __all_sync(ALL, sm100::mbar_wait(full + place_out, phases >> place_out & 1));
+            if (alive) {
+                phases ^= 1u << place_out;
+                pending &= ~(1u << place_out);
+            }
+        }
+        uint8_t *at = ring + place_out * PLACE;
+        if (++place_out == ST) place_out = 0;
+        return at;
+    }
+    // The new token's row of a place is stale: the caller's k or v takes its
+    // place (zeros past d, as in a copy), and goes to its row of the pool.
+    __device__ __forceinline__ void patch(uint8_t *dst, const T *src, T *pool, int d, int blocks, const PagedTile &t)
+    {
+        const int s = t.n - 1 - (t.tile * 4 + warp) * SLOTS;
+        constexpr int PE = 16 / sizeof(E);   // elements of a 16-byte piece
+        for (int i = lane; i < blocks * 8; i += 32) {
+            E x[PE];
+#pragma unroll
+            for (int e = 0; e < PE; ++e) x[e] = E(0.f);
+            if constexpr (TMA) {
+                if (i * PE < d) *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(src + i * PE);
+                if (i * PE < d && t.sub == 0)
+                    *reinterpret_cast<uint4 *>(pool + (size_t)t.newrow * d + i * PE) = *reinterpret_cast<const uint4 *>(x);
+            } else {
+#pragma unroll
+                for (int e = 0; e < PE; ++e)
+                    if (i * PE + e < d) {
+                        const T y = src[i * PE + e];
+                        x[e] = E(ld(&y));
+                        if (t.sub == 0) pool[(size_t)t.newrow * d + i * PE + e] = y;
+                    }
+            }
+            *reinterpret_cast<uint4 *>(dst + (i >> 3) * BLOCK + s * 128 + (((i ^ s) & 7) << 4)) = *reinterpret_cast<const uint4 *>(x);
+        }
+        if (TMA) sm100::fence_proxy_async();   // before a later copy writes this place
+        __syncwarp();
+    }
+    __device__ __forceinline__ PagedTile tile(int it) const
+    {
+        const int4 *from = reinterpret_cast<const int4 *>(tiles_at + it % kPagedAhead);
+        const int4 x = from[0], y = from[1];
+        PagedTile t;
+        t.mask = (uint32_t)x.x;
+        t.copies = (uint32_t)x.y;
+        t.newrow = x.z;
+        t.n = x.w;
+        t.b = y.x;
+        t.h = y.y;
+        t.sub = y.z;
+        t.tile = y.w;
+        return t;
+    }
+    // after a wait that ran out, let this warp's own copies land before leaving (bounded)
+    __device__ __forceinline__ void drain()
+    {
+        if (TMA && !alive)
+            for (int i = 0; i < ST; ++i)
+                if (pending >> i & 1) sm100::mbar_wait(full + i, phases >> i & 1, 100000000ull);
+    }
+};
+
+__device__ __forceinline__ PagedWalk paged_unit(const PagedDecodeParams &p, const PagedTile &t)
+{
+    PagedWalk w;
+    w.b = t.b;
+    w.h = t.h;
+    w.sub = t.sub;
+    w.tile = t.tile;
+    w.set(p, t.n);
+    return w;
+}
+
+// The new token's position goes beside its slot.
+__device__ __forceinline__ void paged_store_position(const PagedDecodeParams &p, const PagedWalk &w)
+{
+    if (p.positions && threadIdx.x == 0 && w.sub == 0 && w.n > 0 && w.tile == w.nt - 1 &&
+        paged_row(p.c, w.b, w.h, w.n - 1) >= 0)
+        p.positions[w.bh(p) * p.c.cap() + w.n - 1] = p.pos[w.b];
+}
+
+// A permutation of 0..7: the slot (of eight) whose key thread lane / 4 reads.
+// With the swizzle it lets the reads of both kernels touch every bank once:
+// eight lanes read 16 bytes each at a time, and they are rows slot(2i),
+// slot(2i+1) (which differ in bit 2) for keys, and rows slot(0), slot(2),
+// slot(4), slot(6) (which differ above bit 0) for the values of the MMA kernel.
+__device__ __forceinline__ int paged_slot(int r)
+{
+    return ((r ^ r >> 2) & 1) << 2 | (r & 2) | r >> 2;
+}
+
 // bf16, dqk and dv multiples of 8, on the tensor cores with mma.sync: the work
 // per byte (2 * heads FLOP) is far below what a tcgen05 tile is for, and its 16
-// rows hold the query heads.  Each warp brings the keys, then the values, of its
-// next 32 slots into its own ring of shared memory by TMA, `ST` loads deep, with
-// one mbarrier per place: slots of a page are neighbouring rows of the pool, so a
-// box of `box_rows` rows (32, 16, 8 or 4, whichever divides the page size) and 64
-// columns is one copy; pages of other sizes gather four rows by index.  Nothing
-// but the wait for its own copies orders a warp inside a unit.
+// rows hold the query heads.
 //
 // The operands go from shared memory to the MMA's registers without a
 // transpose, because a sum does not depend on the order of its terms and a
@@ -434,32 +651,23 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
 //   O = P V    thread (r, c) reads the values 64 j + 8 r .. + 7 of the slots
 //       slot(2c), slot(2c+1) (+ 8 i): a byte permutation pairs two slots, and
 //       column block e of the product is the values 64 j + 8 r + e.
-// The permutation slot() of 0..7 lets both reads touch every bank once: a copy
-// stores 16-byte piece i of row t at piece i ^ (t mod 8), eight lanes read at a
-// time, and they are rows slot(2i), slot(2i+1) (which differ in bit 2) for K and
-// rows slot(0), slot(2), slot(4), slot(6) (which differ above bit 0) for V.
-//
 // P enters as two bf16 halves, p = hi + lo (error 2^-17 of p instead of 2^-9).
 // With at most 8 heads (HI false) the low half takes the rows 8..15, which are
 // free, and costs no further MMA.
 template <int DQ, int DV, bool HI>
 struct PagedMma {
     static constexpr int KB = DQ / 64, VB = DV / 64;           // 64-column blocks
-    static constexpr int BLOCK = 32 * 128;                     // 32 slots x 128 bytes
-    static constexpr int PLACE = (KB > VB ? KB : VB) * BLOCK;  // one load: a warp's keys or values
-    static constexpr int ST = PLACE > BLOCK ? 3 : 4;
-    static constexpr int OFF_O = kPagedWarps * ST * PLACE;
+    static constexpr int ST = KB > 1 || VB > 1 ? 3 : 4;
+    using Feed = PagedFeed<__nv_bfloat16, __nv_bfloat16, KB, VB, 32, ST, true>;
+    static constexpr int BLOCK = Feed::BLOCK;
+    static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
     static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * DV * 4;
-    static constexpr int OFF_BAR = OFF_ML + kPagedWarps * kPagedRows * 8;
-    static constexpr int OFF_MASK = OFF_BAR + kPagedWarps * ST * 8;      // [warp][4] (slots attended to, copies made)
-    static constexpr int SMEM = OFF_MASK + kPagedWarps * 4 * 8;
-    static constexpr int BLOCKS = PLACE > BLOCK ? 2 : 3;       // per SM
+    static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
+    static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * (int)sizeof(PagedTile);
+    static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
+    static constexpr int BLOCKS = KB > 1 || VB > 1 ? 2 : 3;    // per SM
+    static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
-
-__device__ __forceinline__ int paged_slot(int r)
-{
-    return ((r ^ r >> 2) & 1) << 2 | (r & 2) | r >> 2;
-}
 
 template <int DQ, int DV, bool HI>
 __global__ void __launch_bounds__(kPagedThreads, PagedMma<DQ, DV, HI>::BLOCKS)
@@ -470,14 +678,12 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     using T = __nv_bfloat16;
     using namespace sm100;
     constexpr uint32_t ALL = 0xffffffffu;
-    extern __shared__ __align__(1024) uint8_t smem[];   // SW128 tiles from the start; no static shared memory before it
+    extern __shared__ __align__(1024) uint8_t smem[];   // swizzled tiles from the start; no static shared memory before it
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
     float *obuf = reinterpret_cast<float *>(smem + Cfg::OFF_O);
     float2 *mls = reinterpret_cast<float2 *>(smem + Cfg::OFF_ML);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR) + warp * Cfg::ST;
-    uint2 *masks = reinterpret_cast<uint2 *>(smem + Cfg::OFF_MASK) + warp * 4;
-    uint8_t *ring = smem + warp * Cfg::ST * Cfg::PLACE;
     if (lane == 0) {
         for (int i = 0; i < Cfg::ST; ++i) mbar_init(full + i, 1);
         mbar_init_fence();
@@ -495,86 +701,10 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     if (tid == 0) paged_record(p, w, tiles, chunk);
     if (!tiles) return;
     __syncthreads();   // the barriers are set, and the record is written before paged_part adds to it
-
-    // Loads, keys and values of a tile in turn.  `lw` is the tile whose loads are
-    // next and `page` its table entries, one slot per lane.  Slots past the end
-    // and on bad pages are not brought in: what their rows hold is masked.
-    PagedWalk lw = w;
-    auto slot_in = [&]() { return (lw.tile << 7) + warp * 32 + lane; };
-    int issued = 0, place_in = 0, page = paged_entry(p, lw, slot_in()), row = 0;
-    uint32_t copies = 0, pending = 0, phases = 0;
-    bool alive = true;          // false once a wait ran out: no more loads, no more work
-    const int group = p.box_rows < 4 ? 4 : p.box_rows;         // slots per copy
-    const uint32_t group_mask = group == 32 ? ALL : (1u << group) - 1;
-    auto issue = [&]() {
-        if (issued >= 2 * tiles || !alive) return;
-        const bool isv = issued & 1;
-        if (!isv) {
-            row = paged_entry_row(p, lw, slot_in(), page);
-            const uint32_t mask = __ballot_sync(ALL, row != kPagedNone);   // slots attended to
-            const uint32_t held = __ballot_sync(ALL, row >= 0);            // of them, in the pool
-            // a box lies in one page: its first slot is held if any is; four gathered
-            // rows are brought in if any is held (row 0 in place of the others)
-            copies = __ballot_sync(ALL, (lane & (group - 1)) == 0 && (held >> lane & group_mask));
-            if (lane == 0) masks[issued >> 1 & 3] = make_uint2(mask, copies);
-            if ((issued >> 1) + 1 < tiles) {
-                lw.next(p);
-                page = paged_entry(p, lw, slot_in());
-            }
-        }
-        if (copies) {
-            const CUtensorMap *map = isv ? &tm_v : &tm_k;
-            if (lane == 0)
-                mbar_arrive_expect_tx(full + place_in, __popc(copies) * group * 128 * (isv ? Cfg::VB : Cfg::KB));
-            int y1, y2, y3;
-            if (p.box_rows < 4) {
-                y1 = max(__shfl_down_sync(ALL, row, 1), 0);
-                y2 = max(__shfl_down_sync(ALL, row, 2), 0);
-                y3 = max(__shfl_down_sync(ALL, row, 3), 0);
-            }
-            __syncwarp();
-            if (copies >> lane & 1) {
-                uint8_t *dst = ring + place_in * Cfg::PLACE + lane * 128;
-#pragma unroll
-                for (int j = 0; j < (Cfg::KB > Cfg::VB ? Cfg::KB : Cfg::VB); ++j) {
-                    if (j >= (isv ? Cfg::VB : Cfg::KB)) break;
-                    if (p.box_rows < 4)
-                        tma_gather4(dst + j * Cfg::BLOCK, map, full + place_in, j * 64, max(row, 0), y1, y2, y3);
-                    else
-                        tma_load_2d(dst + j * Cfg::BLOCK, map, full + place_in, j * 64, row);
-                }
-            }
-            pending |= 1u << place_in;
-        }
-        ++issued;
-        if (++place_in == Cfg::ST) place_in = 0;
-    };
-    // the next place of the ring, once its copies have landed
-    int place = 0;
-    auto take = [&](bool copied) {
-        if (copied && alive) {
-            alive = __all_sync(ALL, mbar_wait(full + place, phases >> place & 1));
-            if (alive) {
-                phases ^= 1u << place;
-                pending &= ~(1u << place);
-            }
-        }
-        uint8_t *at_place = ring + place * Cfg::PLACE;
-        if (++place == Cfg::ST) place = 0;
-        return at_place;
-    };
-    // The new token's row of a place is stale: the caller's k or v takes its
-    // place (zeros past d, as in a copy).
-    auto patch = [&](uint8_t *dst, const T *src, int d, int blocks, int slot) {
-        if (lane < blocks * 8) {
-            const uint4 x = lane * 8 < d ? *reinterpret_cast<const uint4 *>(src + lane * 8) : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(dst + (lane >> 3) * Cfg::BLOCK + slot * 128 + (((lane ^ slot) & 7) << 4)) = x;
-        }
-        fence_proxy_async();   // before a later copy writes this place
-        __syncwarp();
-    };
+    typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::ST * Cfg::Feed::PLACE, full,
+                            reinterpret_cast<PagedTile *>(smem + Cfg::OFF_TILE) + warp * kPagedAhead, w, tiles);
 #pragma unroll 1
-    for (int s = 0; s < Cfg::ST - 1; ++s) issue();
+    for (int s = 0; s < Cfg::ST - 1; ++s) feed.issue();
 
     const int sk = paged_slot(r), sv0 = paged_slot(2 * cq), sv1 = paged_slot(2 * cq + 1);
     const uint32_t off_k = sk * 128 + ((cq ^ sk) << 4);   // coordinates 32 j + ..: ^ 64 for odd j, + a block per two
@@ -583,22 +713,26 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     constexpr int NR = HI ? 2 : 1;   // rows of a thread: r and r + 8
     uint4 qf[DQ / 32][NR];
     float o[DV / 8][4], m[NR], l[NR];
-    int t0 = 0, rows = 0;
-    size_t hq0 = 0;
+    auto load_q = [&](const PagedWalk &u) {
+        const int rows = u.rows(p);
+        const T *q = (const T *)p.q + u.hq(p) * c.dqk;
+#pragma unroll
+        for (int j = 0; j < DQ / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int col = j * 32 + cq * 8, row = r + 8 * i;
+                qf[j][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row < rows && col < c.dqk) qf[j][i] = *reinterpret_cast<const uint4 *>(q + row * c.dqk + col);
+            }
+    };
+    load_q(w);
+    int t0 = 0;
     for (int it = 0; it < tiles; ++it) {
+        __syncwarp();
+        const PagedTile t = feed.tile(it);
+        w = paged_unit(p, t);
         if (it == 0 || w.tile == 0) {   // a new unit
             t0 = w.tile;
-            rows = w.rows(p);
-            hq0 = w.hq(p);
-#pragma unroll
-            for (int j = 0; j < DQ / 32; ++j)
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    const int col = j * 32 + cq * 8, row_q = r + 8 * i;
-                    qf[j][i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row_q < rows && col < c.dqk)
-                        qf[j][i] = *reinterpret_cast<const uint4 *>((const T *)p.q + (hq0 + row_q) * c.dqk + col);
-                }
 #pragma unroll
             for (int i = 0; i < DV / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
@@ -607,21 +741,22 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 l[i] = 0.f;
             }
         }
-        __syncwarp();
-        const uint2 mk = masks[it & 3];
-        const bool copied = mk.y != 0;
-        const uint32_t mask = mk.x;
-        float *const sc = p.scores ? p.scores + (hq0 + r) * p.stride + (w.tile << 7) + warp * 32 : nullptr;
-        const int last = p.k ? w.n - 1 - ((w.tile << 7) + warp * 32) : -1;   // the new token's slot in this chunk
-        const bool fresh = last >= 0 && last < 32 && (mask >> last & 1);
+        const uint32_t mask = t.mask;
+        const int rows = w.rows(p);
+        float *const sc = p.scores ? p.scores + (w.hq(p) + r) * p.stride + (w.tile << 7) + warp * 32 : nullptr;
+        uint8_t *kp = feed.take(t.copies);
+        feed.issue();   // into the place before, which every lane has used; with it the next tile is known
+        // the next unit's queries are on their way while this one is finished
+        auto next_q = [&]() {
+            if (it + 1 >= tiles || w.tile != w.nt - 1) return;
+            __syncwarp();
+            load_q(paged_unit(p, feed.tile(it + 1)));
+        };
 
         // one tile; `whole`: every slot is attended to
         auto work = [&](auto whole_tag) {
             constexpr bool WHOLE = decltype(whole_tag)::value;
-            uint8_t *kp = take(copied);
-            issue();   // into the place before, which every lane has used
-            if (!alive) return;
-            if (fresh) patch(kp, (const T *)p.k + w.bh(p) * c.dqk, c.dqk, Cfg::KB, last);
+            if (t.newrow >= 0) feed.patch(kp, (const T *)p.k + w.bh(p) * c.dqk, (T *)c.kp, c.dqk, Cfg::KB, t);
             const uint32_t ks = smem_addr(kp);
             float s[4][4];
 #pragma unroll
@@ -637,6 +772,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mma_16816(s[i], a.z, b.z, a.w, b.w, kk[i].z, kk[i].w);
             }
+            next_q();
             // scores in log2 units; slot of s[i][e] (and s[i][e + 2]): 8 i + sv_e
             float mn[NR];
 #pragma unroll
@@ -693,10 +829,10 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 }
                 l[n] += sum;
             }
-            uint8_t *vp = take(copied);
-            issue();
-            if (!alive) return;
-            if (fresh) patch(vp, (const T *)p.v + w.bh(p) * c.dv, c.dv, Cfg::VB, last);
+            uint8_t *vp = feed.take(t.copies);
+            feed.issue();
+            if (!feed.alive) return;
+            if (t.newrow >= 0) feed.patch(vp, (const T *)p.v + w.bh(p) * c.dv, (T *)c.vp, c.dv, Cfg::VB, t);
             const uint32_t vs = smem_addr(vp);
 #pragma unroll
             for (int j = 0; j < DV / 64; ++j) {
@@ -727,9 +863,9 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 }
             }
         };
-        if (mask == ALL) {
+        if (mask == ALL && feed.alive) {
             work(std::true_type{});
-        } else if (mask) {
+        } else if (mask && feed.alive) {
             work(std::false_type{});
         } else {   // slots past the end, or on bad pages: no weight
             if (sc && w.n > 0)
@@ -739,10 +875,9 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             sc[8 * n * p.stride + 8 * i + sv0] = sc[8 * n * p.stride + 8 * i + sv1] = -INFINITY;
-            take(false);
-            issue();
-            take(false);
-            issue();
+            next_q();
+            feed.take(false);
+            feed.issue();
         }
         if (w.tile == w.nt - 1 || it == tiles - 1) {   // the unit, or its part in this range, ends
             bool whole;
@@ -774,78 +909,54 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                                 to[j * 16 + e * 2 + f] = make_float4(x[0], x[1], x[2], x[3]);
                             }
                     __syncthreads();
-                    paged_merge<T, DV>(p, w, obuf, mls, 8 * n, rows, whole, slot);
+                    paged_merge<T, DV, 8>(p, w, obuf, mls, 8 * n, rows, whole, slot);
                     __syncthreads();
                 }
-                if (p.k && w.sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
+                paged_store_position(p, w);
             }
         }
-        if (it < tiles - 1) w.next(p);
     }
-    // after a wait that ran out, let this warp's own copies land before leaving (bounded)
-    if (!alive)
-        for (int i = 0; i < Cfg::ST; ++i)
-            if (pending >> i & 1) mbar_wait(full + i, phases >> i & 1, 100000000ull);
+    feed.drain();
 }
 
 // fp32, and bf16 rows that do not start on 16-byte boundaries: the same walk
-// with fp32 FMA.  A quad of lanes shares a slot in the scores (lane c holds the
-// coordinates 16 j + 4 c .. + 3 of slots r and r + 8), and a lane owns four
-// columns of the output.  Rows reach the thread that uses them through its own
-// 16-byte slots of shared memory as above, as four floats each.
-template <typename T, int D, int GM>
+// with fp32 FMA on four floats per 16-byte piece.  A quad of lanes shares a slot
+// in the scores (lane c holds the coordinates 16 j + 4 c .. + 3 of slots slot(r)
+// and 8 + slot(r)), and a lane owns four columns of the output.
+template <typename T, int D, int GM, bool TMA>
 struct PagedSimt {
-    static constexpr int KP = D / 8;                 // pieces per thread and tile: 2 slots x D / 16
+    static constexpr int NB = D / 32;                // 32-column blocks
+    static constexpr int ST = D > 64 && GM > 4 ? 2 : 3;
+    static constexpr int OR = GM < 8 ? GM : 8;       // rows merged at once
+    using Feed = PagedFeed<T, float, NB, NB, 16, ST, TMA>;
+    static constexpr int BLOCK = Feed::BLOCK;
     static constexpr int LR = D / 4, TP = 32 / LR;   // lanes per value row, rows per pass
-    static constexpr int VP = 16 / TP;
-    static constexpr int STAGE = (KP + VP) * 16 * kPagedThreads;
-    static constexpr int ST = D > 64 ? 2 : 3;
-    static constexpr int OFF_O = ST * STAGE;
-    static constexpr int OFF_Q = OFF_O + kPagedWarps * 8 * D * 4;          // [16][D] queries, shared by the warps
+    static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
+    static constexpr int OFF_Q = OFF_O + kPagedWarps * OR * D * 4;         // [GM][D] queries, shared by the warps
     static constexpr int OFF_P = OFF_Q + GM * D * 4;                       // [warp][16][GM] weights
     static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
-    static constexpr int OFF_MASK = OFF_ML + kPagedWarps * kPagedRows * 8;
-    static constexpr int SMEM = OFF_MASK + kPagedWarps * ST * 4;
-    static constexpr int BLOCKS = D > 64 ? 1 : 2;
+    static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
+    static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * (int)sizeof(PagedTile);
+    static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
+    static constexpr int BLOCKS = D > 64 || GM > 4 ? 2 : 3;                // per SM
+    static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-// Four elements of a row (those below d; zeros after) into a 16-byte slot.
-template <typename T>
-__device__ __forceinline__ void paged_load4(uint32_t dst, const T *row, int col, int d, bool live, bool vec)
-{
-    if constexpr (sizeof(T) == 4) {
-        if (vec) {
-            const bool ok = live && col < d;
-            cp_async16(dst, ok ? row + col : row, ok);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool ok = live && col + e < d;
-                cp_async4(dst + 4 * e, ok ? row + col + e : row, ok);
-            }
-        }
-    } else {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = live && col + e < d ? ld(row + col + e) : 0.f;
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
-                     : "memory");
-    }
-}
 __device__ __forceinline__ float4 lds_f4(uint32_t a)
 {
     const uint4 v = lds128(a);
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-template <typename T, int D, int GM>
-__global__ void __launch_bounds__(kPagedThreads, PagedSimt<T, D, GM>::BLOCKS)
-paged_decode_simt_kernel(const PagedDecodeParams p)
+template <typename T, int D, int GM, bool TMA>
+__global__ void __launch_bounds__(kPagedThreads, PagedSimt<T, D, GM, TMA>::BLOCKS)
+paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const PagedDecodeParams p)
 {
-    using Cfg = PagedSimt<T, D, GM>;
+    using Cfg = PagedSimt<T, D, GM, TMA>;
+    using namespace sm100;
+    constexpr uint32_t ALL = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t smem[];
-    sm100::grid_dependency_wait();
-    sm100::launch_dependents();
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cq = lane & 3;
     const int vcol = (lane % Cfg::LR) * 4, vrow = lane / Cfg::LR;
@@ -853,8 +964,17 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
     float *qs = reinterpret_cast<float *>(smem + Cfg::OFF_Q);
     float *ps = reinterpret_cast<float *>(smem + Cfg::OFF_P) + warp * 16 * GM;
     float2 *mls = reinterpret_cast<float2 *>(smem + Cfg::OFF_ML);
-    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MASK) + warp * Cfg::ST;
-    const uint32_t ring = sm100::smem_addr(smem) + tid * 16;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR) + warp * Cfg::ST;
+    if (TMA && lane == 0) {
+        for (int i = 0; i < Cfg::ST; ++i) mbar_init(full + i, 1);
+        mbar_init_fence();
+        if (warp == 0) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+        }
+    }
+    grid_dependency_wait();
+    launch_dependents();
 
     PagedWalk w;
     long long at, chunk;
@@ -862,53 +982,21 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
     if (tid == 0) paged_record(p, w, tiles, chunk);
     if (!tiles) return;
     __syncthreads();
+    typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::ST * Cfg::Feed::PLACE, full,
+                            reinterpret_cast<PagedTile *>(smem + Cfg::OFF_TILE) + warp * kPagedAhead, w, tiles);
+#pragma unroll 1
+    for (int s = 0; s < Cfg::ST - 1; ++s) feed.issue();
 
-    PagedWalk lw = w;
-    // slot of this lane (lanes 0..15) in the tile whose loads are next
-    auto slot_in = [&]() { return lane < 16 ? (lw.tile << 6) + warp * 16 + lane : INT_MAX; };
-    auto entry = [&]() { return paged_entry(p, lw, slot_in()); };
-    int issued = 0, page = entry();
-    auto issue = [&]() {
-        if (issued < tiles) {
-            const int stage = issued % Cfg::ST;
-            const int row = paged_entry_row(p, lw, slot_in(), page);
-            const uint32_t mask = __ballot_sync(0xffffffffu, row != kPagedNone);
-            if (lane == 0) masks[stage] = mask;
-            if (mask) {
-                const size_t bh = lw.bh(p);
-                const uint32_t dst = ring + stage * Cfg::STAGE;
-                const T *kn = (const T *)p.k + bh * c.dqk, *vn = (const T *)p.v + bh * c.dv;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rw = __shfl_sync(0xffffffffu, row, i * 8 + r);
-                    const T *src = rw == kPagedNew ? kn : (const T *)c.kp + (size_t)max(rw, 0) * c.dqk;
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        if (j * 16 < c.dqk)
-                            paged_load4(dst + (i * (D / 16) + j) * (16 * kPagedThreads), src, j * 16 + cq * 4, c.dqk,
-                                        rw != kPagedNone, p.vec);
-                }
-#pragma unroll
-                for (int i = 0; i < Cfg::VP; ++i) {
-                    const int rw = __shfl_sync(0xffffffffu, row, i * Cfg::TP + vrow);
-                    const T *src = rw == kPagedNew ? vn : (const T *)c.vp + (size_t)max(rw, 0) * c.dv;
-                    paged_load4(dst + (Cfg::KP + i) * (16 * kPagedThreads), src, vcol, c.dv, rw != kPagedNone, p.vec);
-                }
-            }
-            if (++issued < tiles) {
-                lw.next(p);
-                page = entry();
-            }
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < Cfg::ST - 1; ++s) issue();
-
+    const int sk = paged_slot(r);
+    const uint32_t off_k = sk * 128 + ((cq ^ sk) << 4);   // coordinates 16 j + ..: ^ 64 for odd j, + a block per two
+    const uint32_t off_v = (vcol / 32) * Cfg::BLOCK;
     float4 o[GM];
     float m[GM], l[GM];
     int t0 = 0;
     for (int it = 0; it < tiles; ++it) {
+        __syncwarp();
+        const PagedTile t = feed.tile(it);
+        w = paged_unit(p, t);
         const int rows = w.rows(p);
         const size_t hq0 = w.hq(p);
         if (it == 0 || w.tile == 0) {
@@ -926,21 +1014,20 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
                 l[n] = 0.f;
             }
         }
-        cp_async_wait<Cfg::ST - 2>();
-        __syncwarp();
-        const int stage = it % Cfg::ST;
-        const uint32_t mask = masks[stage];
-        issue();
-        if (mask) {
-            const uint32_t src = ring + stage * Cfg::STAGE;
+        const uint32_t mask = t.mask;
+        uint8_t *kp = feed.take(t.copies);
+        feed.issue();
+        if (mask && feed.alive) {
+            if (t.newrow >= 0) feed.patch(kp, (const T *)p.k + w.bh(p) * c.dqk, (T *)c.kp, c.dqk, Cfg::NB, t);
+            const uint32_t ks = smem_addr(kp);
             float s[2][GM];
 #pragma unroll
             for (int n = 0; n < GM; ++n) s[0][n] = s[1][n] = 0.f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 if (j * 16 >= c.dqk) break;
-                const float4 k0 = lds_f4(src + j * (16 * kPagedThreads));
-                const float4 k1 = lds_f4(src + (D / 16 + j) * (16 * kPagedThreads));
+                const float4 k0 = lds_f4(ks + (j >> 1) * Cfg::BLOCK + (off_k ^ (j & 1) * 64));
+                const float4 k1 = lds_f4(ks + (j >> 1) * Cfg::BLOCK + 1024 + (off_k ^ (j & 1) * 64));
 #pragma unroll
                 for (int n = 0; n < GM; ++n) {
                     if (n >= rows) break;
@@ -949,7 +1036,6 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
                     s[1][n] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[1][n]))));
                 }
             }
-            float al[GM];
 #pragma unroll
             for (int n = 0; n < GM; ++n) {
                 if (n >= rows) break;
@@ -957,50 +1043,59 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float x = s[i][n];
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    s[i][n] = x = mask >> (i * 8 + r) & 1 ? x : -INFINITY;
+                    x += __shfl_xor_sync(ALL, x, 1);
+                    x += __shfl_xor_sync(ALL, x, 2);
+                    s[i][n] = x = mask >> (i * 8 + sk) & 1 ? x : -INFINITY;
                     mx = fmaxf(mx, x);
-                    if (p.scores && cq == 0)
-                        p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + r] = x;
+                    if (p.scores && cq == 0) p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + sk] = x;
                 }
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float base = mx == -INFINITY ? 0.f : mx;
-                al[n] = ex2(m[n] - base);
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, off));
+                const float base = mx == -INFINITY ? 0.f : mx, al = ex2(m[n] - base);
                 m[n] = mx;
                 const float e0 = ex2(s[0][n] - base), e1 = ex2(s[1][n] - base);
-                l[n] = l[n] * al[n] + e0 + e1;
+                l[n] = l[n] * al + e0 + e1;
                 if (cq == (n & 3)) {
-                    ps[r * GM + n] = e0;
-                    ps[(8 + r) * GM + n] = e1;
+                    ps[sk * GM + n] = e0;
+                    ps[(8 + sk) * GM + n] = e1;
                 }
-                o[n].x *= al[n];
-                o[n].y *= al[n];
-                o[n].z *= al[n];
-                o[n].w *= al[n];
+                o[n].x *= al;
+                o[n].y *= al;
+                o[n].z *= al;
+                o[n].w *= al;
             }
             __syncwarp();
+            uint8_t *vp = feed.take(t.copies);
+            feed.issue();
+            if (t.newrow >= 0 && feed.alive) feed.patch(vp, (const T *)p.v + w.bh(p) * c.dv, (T *)c.vp, c.dv, Cfg::NB, t);
+            const uint32_t vs = smem_addr(vp) + off_v;
+            if (feed.alive)
 #pragma unroll
-            for (int i = 0; i < Cfg::VP; ++i) {
-                const float4 x = lds_f4(src + (Cfg::KP + i) * (16 * kPagedThreads));
-                const float *pp = ps + (i * Cfg::TP + vrow) * GM;
+                for (int i = 0; i < 16 / Cfg::TP; ++i) {
+                    const int row = i * Cfg::TP + vrow;
+                    float4 x = lds_f4(vs + row * 128 + (((lane ^ row) & 7) << 4));
+                    // a masked slot's weight is 0, but its row may hold anything: 0 * NaN is NaN
+                    if (!(mask >> row & 1)) x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float *pp = ps + row * GM;
 #pragma unroll
-                for (int n = 0; n < GM; ++n) {
-                    if (n >= rows) break;
-                    const float f = pp[n];
-                    o[n].x = fmaf(f, x.x, o[n].x);
-                    o[n].y = fmaf(f, x.y, o[n].y);
-                    o[n].z = fmaf(f, x.z, o[n].z);
-                    o[n].w = fmaf(f, x.w, o[n].w);
+                    for (int n = 0; n < GM; ++n) {
+                        if (n >= rows) break;
+                        const float f = pp[n];
+                        o[n].x = fmaf(f, x.x, o[n].x);
+                        o[n].y = fmaf(f, x.y, o[n].y);
+                        o[n].z = fmaf(f, x.z, o[n].z);
+                        o[n].w = fmaf(f, x.w, o[n].w);
+                    }
                 }
-            }
-        } else if (p.scores && w.n > 0 && cq == 0) {
-            for (int n = 0; n < rows; ++n)
-                for (int i = 0; i < 2; ++i)
-                    p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + r] = -INFINITY;
+            __syncwarp();   // the weights are read before the next tile's
+        } else {
+            if (p.scores && w.n > 0 && cq == 0)
+                for (int n = 0; n < rows; ++n)
+                    for (int i = 0; i < 2; ++i)
+                        p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + r] = -INFINITY;
+            feed.take(false);
+            feed.issue();
         }
-        __syncwarp();   // the weights are read before the next tile's
         if (w.tile == w.nt - 1 || it == tiles - 1) {
             bool whole;
             const int slot = paged_part(p, w, t0, at + it, whole);
@@ -1010,12 +1105,12 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
 #pragma unroll
                 for (int n = 0; n < GM; ++n) {   // a slot's weight is held by its quad's four lanes alike
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], off);
+                    for (int off = 4; off < 32; off <<= 1) l[n] += __shfl_xor_sync(ALL, l[n], off);
                     if (Cfg::TP == 2) {
-                        o[n].x += __shfl_xor_sync(0xffffffffu, o[n].x, 16);
-                        o[n].y += __shfl_xor_sync(0xffffffffu, o[n].y, 16);
-                        o[n].z += __shfl_xor_sync(0xffffffffu, o[n].z, 16);
-                        o[n].w += __shfl_xor_sync(0xffffffffu, o[n].w, 16);
+                        o[n].x += __shfl_xor_sync(ALL, o[n].x, 16);
+                        o[n].y += __shfl_xor_sync(ALL, o[n].y, 16);
+                        o[n].z += __shfl_xor_sync(ALL, o[n].z, 16);
+                        o[n].w += __shfl_xor_sync(ALL, o[n].w, 16);
                     }
                     if (lane == 0) mls[warp * kPagedRows + n] = make_float2(m[n], l[n]);
                 }
@@ -1023,17 +1118,16 @@ paged_decode_simt_kernel(const PagedDecodeParams p)
                 for (int n0 = 0; n0 < GM; n0 += 8) {
 #pragma unroll
                     for (int n = n0; n < GM && n < n0 + 8; ++n)
-                        if (vrow == 0) *reinterpret_cast<float4 *>(obuf + (warp * 8 + n - n0) * D + vcol) = o[n];
+                        if (vrow == 0) *reinterpret_cast<float4 *>(obuf + (warp * Cfg::OR + n - n0) * D + vcol) = o[n];
                     __syncthreads();
-                    paged_merge<T, D>(p, w, obuf, mls, n0, min(rows, GM), whole, slot);
+                    paged_merge<T, D, Cfg::OR>(p, w, obuf, mls, n0, min(rows, GM), whole, slot);
                     __syncthreads();
                 }
-                if (p.k && w.sub == 0 && w.tile == w.nt - 1) paged_store_new<T>(p, w);
+                paged_store_position(p, w);
             }
         }
-        if (it < tiles - 1) w.next(p);
     }
-    cp_async_wait<0>();
+    feed.drain();
 }
 
 // Maximum and sum of row `row` over the parts of a unit that crosses ranges.
@@ -1123,7 +1217,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
     w.h = rec.u / p.nsub;
     w.sub = rec.u - w.h * p.nsub;
     w.tile = rec.tile;
-    w.load(p);
+    w.set(p, paged_count(p, w.b));
     long long at = blockIdx.x * rec.chunk;
     for (int left = rec.tiles; left > 0;) {
         const int here = min(left, w.nt - w.tile);
@@ -1180,7 +1274,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
         at += here;
         if (left > 0) {
             w.tile += here - 1;
-            w.next(p);
+            w.next(p, [&](int b) { return paged_count(p, b); });
         }
     }
 }
