@@ -44,6 +44,9 @@ LA_BF16 = 1
 STATUS_NAMES = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_CUDA",
                 4: "LA_ERR_TIMEOUT", 5: "LA_ERR_DEVICE_CHECK", 6: "LA_ERR_SCRATCH_LIMIT"}
 
+# The current stream's handle, without a Stream object where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libla.so")
 _lib = None
@@ -142,9 +145,14 @@ def _call(fn, where, device, *args):
     """One library call for tensors on `device`: that device is made current
     for the call (the library launches on the current device) and its
     current stream is passed as the last argument."""
-    with torch.cuda.device(device):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        _check(fn(*args, stream), where)
+    index = device.index
+    if index is not None and index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(torch.cuda.current_device()))
+    if status:
+        _check(status, where)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -461,16 +469,49 @@ def la_swa_decode_step(q, k, v, k_cache, v_cache, pos, window, y=None):
     return y
 
 
+_paged_sizes = {}   # workspace sizes by their arguments: asked for at every step
+
+
+def _paged_workspace(fn, workspace, device, *sizes):
+    """(pointer, bytes, keep-alive) of the workspace a paged call needs."""
+    need = _paged_sizes.get((fn, sizes))
+    if need is None:
+        need = _paged_sizes[(fn, sizes)] = int(getattr(load_library(), fn)(*sizes))
+    if workspace is None and not need:
+        return None, 0, None
+    workspace, have = _workspace(workspace, need, device)
+    return workspace.data_ptr(), have, workspace
+
+
+def _pointers(device, args):
+    """Device pointers of (name, tensor or None, shape, dtype) after the checks of
+    _expect and _dev: a step checks a dozen tensors, so the common case is one
+    pass, and the messages are those of the two functions."""
+    index, out = device.index, []
+    for _, t, shape, dtype in args:
+        if t is None:
+            out.append(None)
+        elif t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        return out
+    for name, t, shape, dtype in args:
+        _expect(name, t, shape, dtype, device)
+    _dev(*(t for _, t, _, _ in args))
+    raise AssertionError("unreachable: one of the checks above fails")
+
+
 def _paged_cache(k_pages, v_pages, block_table, lens):
-    """Sizes of a paged cache after checking that its four tensors agree:
-    (num_pages, Hkv, page_size, dqk, dv, B, max_pages, dtype code)."""
+    """Sizes of a paged cache and the arguments of its four tensors for _pointers."""
     P, Hkv, page, dqk = k_pages.shape
     dv = v_pages.shape[-1]
     B, max_pages = block_table.shape
-    _expect("v_pages", v_pages, (P, Hkv, page, dv), k_pages.dtype, k_pages.device)
-    _expect("block_table", block_table, (B, max_pages), torch.int32, k_pages.device)
-    _expect("lens", lens, (B,), torch.int32, k_pages.device)
-    return P, Hkv, page, dqk, dv, B, max_pages, _dtype_code(k_pages)
+    dt = k_pages.dtype
+    return P, Hkv, page, dqk, dv, B, max_pages, _dtype_code(k_pages), [
+        ("k_pages", k_pages, (P, Hkv, page, dqk), dt), ("v_pages", v_pages, (P, Hkv, page, dv), dt),
+        ("block_table", block_table, (B, max_pages), torch.int32), ("lens", lens, (B,), torch.int32)]
 
 
 def la_paged_cache_fill(k, v, k_pages, v_pages, block_table, lens, *, n_new=None, weights=None, positions=None,
@@ -481,22 +522,16 @@ def la_paged_cache_fill(k, v, k_pages, v_pages, block_table, lens, *, n_new=None
     int32 [B] (not advanced here).  weights fp32 and positions int32
     [B,Hkv,max_pages*page]: 0 and pos[b] + i are written for the new slots.
     Returns (k_pages, v_pages)."""
-    lib = load_library()
-    P, Hkv, page, dqk, dv, B, max_pages, dt = _paged_cache(k_pages, v_pages, block_table, lens)
-    dev, N = k_pages.device, k.shape[2]
-    slots = (B, Hkv, max_pages * page)
-    _expect("k", k, (B, Hkv, N, dqk), k_pages.dtype, dev)
-    _expect("v", v, (B, Hkv, N, dv), k_pages.dtype, dev)
-    _expect("n_new", n_new, (B,), torch.int32, dev)
-    _expect("weights", weights, slots, torch.float32, dev)
-    _expect("positions", positions, slots, torch.int32, dev)
-    _expect("pos", pos, (B,), torch.int32, dev)
+    P, Hkv, page, dqk, dv, B, max_pages, dt, cache = _paged_cache(k_pages, v_pages, block_table, lens)
+    N, T, slots = k.shape[2], k_pages.dtype, (B, Hkv, max_pages * page)
     if (positions is None) != (pos is None):
         raise ValueError("positions and pos go together")
-    _dev(k, v, k_pages, v_pages, block_table, lens, n_new, weights, positions, pos)
-    _call(lib.la_paged_cache_fill, "la_paged_cache_fill", dev,
-          _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(lens), _ptr(n_new), _ptr(weights),
-          _ptr(positions), _ptr(pos), B, Hkv, N, dqk, dv, P, page, max_pages, dt)
+    kp, vp, tab, ln, k_, v_, nn, w, ps, po = _pointers(k_pages.device, cache + [
+        ("k", k, (B, Hkv, N, dqk), T), ("v", v, (B, Hkv, N, dv), T), ("n_new", n_new, (B,), torch.int32),
+        ("weights", weights, slots, torch.float32), ("positions", positions, slots, torch.int32),
+        ("pos", pos, (B,), torch.int32)])
+    _call(load_library().la_paged_cache_fill, "la_paged_cache_fill", k_pages.device,
+          k_, v_, kp, vp, tab, ln, nn, w, ps, po, B, Hkv, N, dqk, dv, P, page, max_pages, dt)
     return k_pages, v_pages
 
 
@@ -515,10 +550,8 @@ def la_paged_decode_step(q, k, v, k_pages, v_pages, block_table, lens, *, y=None
     receives is added, into weights_out if given, else in place.  positions
     int32 (same shape) with pos int32 [B]: pos[b] is written for the new slot.
     Returns y [B,Hq,dv]."""
-    lib = load_library()
-    P, Hkv, page, dqk, dv, B, max_pages, dt = _paged_cache(k_pages, v_pages, block_table, lens)
-    dev, Hq = q.device, q.shape[1]
-    slots = (B, Hkv, max_pages * page)
+    P, Hkv, page, dqk, dv, B, max_pages, dt, cache = _paged_cache(k_pages, v_pages, block_table, lens)
+    T, Hq, slots, dev = k_pages.dtype, q.shape[1], (B, Hkv, max_pages * page), k_pages.device
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
     if (positions is None) != (pos is None):
@@ -527,25 +560,18 @@ def la_paged_decode_step(q, k, v, k_pages, v_pages, block_table, lens, *, y=None
         raise ValueError("positions need a new token (k, v)")
     if weights_out is not None and weights is None:
         raise ValueError("weights_out needs weights")
-    _expect("q", q, (B, Hq, dqk), k_pages.dtype, k_pages.device)
-    _expect("k", k, (B, Hkv, dqk), q.dtype, dev)
-    _expect("v", v, (B, Hkv, dv), q.dtype, dev)
-    _expect("y", y, (B, Hq, dv), q.dtype, dev)
-    _expect("lse", lse, (B, Hq), torch.float32, dev)
-    _expect("weights", weights, slots, torch.float32, dev)
-    _expect("weights_out", weights_out, slots, torch.float32, dev)
-    _expect("positions", positions, slots, torch.int32, dev)
-    _expect("pos", pos, (B,), torch.int32, dev)
-    wsb = la_paged_decode_workspace_bytes(B, Hq, Hkv, dqk, dv, page, max_pages, weights is not None, dt)
-    workspace, wsb = _workspace(workspace, wsb, dev)
-    _dev(q, k, v, k_pages, v_pages, block_table, lens, y, lse, weights, weights_out, positions, pos)
-    if weights_out is None:
-        weights_out = weights
+    kp, vp, tab, ln, q_, k_, v_, y_, l_, w, wo, ps, po = _pointers(dev, cache + [
+        ("q", q, (B, Hq, dqk), T), ("k", k, (B, Hkv, dqk), T), ("v", v, (B, Hkv, dv), T), ("y", y, (B, Hq, dv), T),
+        ("lse", lse, (B, Hq), torch.float32), ("weights", weights, slots, torch.float32),
+        ("weights_out", weights_out, slots, torch.float32), ("positions", positions, slots, torch.int32),
+        ("pos", pos, (B,), torch.int32)])
+    ws, wsb, keep = _paged_workspace("la_paged_decode_workspace_bytes", workspace, dev,
+                                     B, Hq, Hkv, dqk, dv, page, max_pages, int(weights is not None), dt)
     if y is None:
-        y = torch.empty(B, Hq, dv, dtype=q.dtype, device=dev)
-    _call(lib.la_paged_decode_step, "la_paged_decode_step", dev,
-          _ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(lse), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(lens),
-          _ptr(weights), _ptr(weights_out), _ptr(positions), _ptr(pos), _ptr(workspace), wsb, B, Hq, Hkv, dqk, dv, P,
+        y = torch.empty((B, Hq, dv), dtype=T, device=dev)
+        y_ = y.data_ptr()
+    _call(load_library().la_paged_decode_step, "la_paged_decode_step", dev,
+          q_, k_, v_, y_, l_, kp, vp, tab, ln, w, w if wo is None else wo, ps, po, ws, wsb, B, Hq, Hkv, dqk, dv, P,
           page, max_pages, dt)
     return y
 
@@ -563,30 +589,21 @@ def la_paged_evict(k_pages, v_pages, block_table, lens, weights, budget, *, rece
     and lens int32 [B] are updated in place unless the *_out tensors are given.
     positions and pos int32 [B] are required when recent > 0.  Returns the new
     lens."""
-    lib = load_library()
-    P, Hkv, page, dqk, dv, B, max_pages, dt = _paged_cache(k_pages, v_pages, block_table, lens)
-    dev, budget, recent = k_pages.device, int(budget), int(recent)
-    slots = (B, Hkv, max_pages * page)
+    P, Hkv, page, dqk, dv, B, max_pages, dt, cache = _paged_cache(k_pages, v_pages, block_table, lens)
+    dev, budget, recent, slots = k_pages.device, int(budget), int(recent), (B, Hkv, max_pages * page)
     if recent > 0 and (positions is None or pos is None):
         raise ValueError("recent > 0 needs positions and pos")
     if positions_out is not None and positions is None:
         raise ValueError("positions_out needs positions")
-    _expect("weights", weights, slots, torch.float32, dev)
-    _expect("weights_out", weights_out, slots, torch.float32, dev)
-    _expect("positions", positions, slots, torch.int32, dev)
-    _expect("positions_out", positions_out, slots, torch.int32, dev)
-    _expect("pos", pos, (B,), torch.int32, dev)
-    _expect("lens_out", lens_out, (B,), torch.int32, dev)
-    workspace, wsb = _workspace(workspace, la_paged_evict_workspace_bytes(B, Hkv, page, max_pages, budget), dev)
-    _dev(k_pages, v_pages, block_table, lens, weights, weights_out, positions, positions_out, pos, lens_out)
-    lens_out = lens if lens_out is None else lens_out
-    weights_out = weights if weights_out is None else weights_out
-    positions_out = positions if positions_out is None else positions_out
-    _call(lib.la_paged_evict, "la_paged_evict", dev,
-          _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(lens), _ptr(lens_out), _ptr(weights),
-          _ptr(weights_out), _ptr(positions), _ptr(positions_out), _ptr(pos), _ptr(workspace), wsb, B, Hkv, dqk, dv,
-          P, page, max_pages, budget, recent, dt)
-    return lens_out
+    kp, vp, tab, ln, w, wo, ps, pso, po, lo = _pointers(dev, cache + [
+        ("weights", weights, slots, torch.float32), ("weights_out", weights_out, slots, torch.float32),
+        ("positions", positions, slots, torch.int32), ("positions_out", positions_out, slots, torch.int32),
+        ("pos", pos, (B,), torch.int32), ("lens_out", lens_out, (B,), torch.int32)])
+    ws, wsb, keep = _paged_workspace("la_paged_evict_workspace_bytes", workspace, dev, B, Hkv, page, max_pages, budget)
+    _call(load_library().la_paged_evict, "la_paged_evict", dev,
+          kp, vp, tab, ln, ln if lo is None else lo, w, w if wo is None else wo, ps, ps if pso is None else pso, po,
+          ws, wsb, B, Hkv, dqk, dv, P, page, max_pages, budget, recent, dt)
+    return lens if lens_out is None else lens_out
 
 
 def la_paged_kernel_plan(op: int, B, Hq, Hkv, dqk, dv, page_size, max_pages, with_weights, dtype):
