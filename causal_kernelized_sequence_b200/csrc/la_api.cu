@@ -1380,8 +1380,12 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
                          : dtype == LA_F32  ? paged_simt<float, false>(p, pl, st)
                                             : paged_simt<__nv_bfloat16, false>(p, pl, st);
     if (s1 != LA_OK || pl.aligned) return s1;
-    if (dtype == LA_F32) return launch_pdl(paged_join_kernel<float>, pl.grid, kPagedJoinThreads, 0, st, p);
-    return launch_pdl(paged_join_kernel<__nv_bfloat16>, pl.grid, kPagedJoinThreads, 0, st, p);
+    const int jg = weights_in ? pl.grid * kPagedWeightBlocks : pl.grid;
+    if (dtype == LA_F32)
+        return weights_in ? launch_pdl(paged_join_kernel<float, true>, jg, kPagedJoinThreads, 0, st, p)
+                          : launch_pdl(paged_join_kernel<float, false>, jg, kPagedJoinThreads, 0, st, p);
+    return weights_in ? launch_pdl(paged_join_kernel<__nv_bfloat16, true>, jg, kPagedJoinThreads, 0, st, p)
+                      : launch_pdl(paged_join_kernel<__nv_bfloat16, false>, jg, kPagedJoinThreads, 0, st, p);
 }
 
 // Most slots that can move in one (b, h): as many as lie below the budget, or above it.

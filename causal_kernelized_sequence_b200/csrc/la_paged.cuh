@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 
 constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
-constexpr int kPagedJoinThreads = 256;
+constexpr int kPagedJoinThreads = 128;     // of the join
+constexpr int kPagedWeightBlocks = 4;      // with weights: blocks of the join per range
 constexpr int kPagedRows = 16;       // query heads of a unit
 constexpr int kPagedMaxGroup = 128;  // query heads per key/value head
 
@@ -246,13 +247,16 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
     const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
     const int slab = (B + kPagedThreads - 1) / kPagedThreads, b0 = min(B, tid * slab), b1 = min(B, b0 + slab);
     long long mine = 0, total;
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) mine += paged_tiles(p, paged_count(p, b));
     long long before = block_scan<kPagedThreads>(mine, part, total);
     total *= U;
-    chunk = (total + gridDim.x - 1) / gridDim.x;
+    const bool small = total < INT_MAX / 2;   // (a 32-bit division is a fraction of a 64-bit one)
+    chunk = small ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     first = blockIdx.x * chunk;
-    const long long x = first / U;
-    if (first < total && x >= before && x < before + mine) {
+    if (first >= total) return 0;
+    const long long x = small ? (unsigned)first / (unsigned)U : first / U;
+    if (x >= before && x < before + mine) {
         int b = b0;
         for (;; ++b) {
             const int nt = paged_tiles(p, paged_count(p, b));
@@ -263,11 +267,10 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
         found[1] = before;
     }
     __syncthreads();
-    if (first >= total) return 0;
     w.b = (int)found[0];
     w.set(p, paged_count(p, w.b));
     const long long off = first - U * found[1];   // below U * nt
-    const int u = (int)(off / w.nt);
+    const int u = small ? (int)((unsigned)off / (unsigned)w.nt) : (int)(off / w.nt);
     w.h = u / p.nsub;
     w.sub = u - w.h * p.nsub;
     w.tile = (int)(off - (long long)u * w.nt);
@@ -288,38 +291,59 @@ __device__ __forceinline__ void paged_record(const PagedDecodeParams &p, const P
     r.tile = w.tile;
 }
 
-// Where one unit's part of a range ends: the four warps' rows r0 .. r0 + OR - 1
-// lie in obuf [warp][OR][DV] and their maxima and sums in mls [warp][16].  Finishes
-// the rows (`whole`) or leaves them to the join as part `slot`.
-template <typename T, int DV, int OR>
-__device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const PagedWalk &w, const float *obuf,
-                                            const float2 *mls, int r0, int rows, bool whole, int slot)
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x)
 {
-    const int tid = threadIdx.x, col = tid % DV;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The merge buffer: [warp][OR rows][64 columns] floats, four columns to a piece.
+// Piece q of row r lies at piece q ^ (q >> 3) ^ 2 (r mod 2): the MMA kernel's
+// threads write pieces 4 c + i (c = lane % 4) of rows 2 k, 2 k + 1 at once, and
+// so touch every bank.
+constexpr int kPagedMergeCols = 64;
+__device__ __forceinline__ int paged_piece(int q, int r) { return q ^ (q >> 3 & 1) ^ (r & 1) << 1; }
+
+// Where one unit's part of a range ends: columns col0 .. col0 + 63 of the four
+// warps' rows r0 .. r0 + OR - 1 lie in obuf and their maxima and sums in mls
+// [warp][16].  Finishes the rows (`whole`) or leaves them to the join as part `slot`.
+template <typename T, int OR>
+__device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const PagedWalk &w, const float *obuf,
+                                            const float2 *mls, int r0, int col0, int rows, bool whole, int slot)
+{
+    const int tid = threadIdx.x, col = tid % kPagedMergeCols;
     const size_t hq0 = w.hq(p);
-    for (int r = tid / DV; r < OR && r0 + r < rows; r += kPagedThreads / DV) {
-        float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPagedWarps; ++i) M = fmaxf(M, mls[i * kPagedRows + r0 + r].x);
+    for (int r = tid / kPagedMergeCols; r < OR; r += kPagedThreads / kPagedMergeCols) {
+        if (r0 + r >= rows) break;
+        float2 e[kPagedWarps];
+        float x[kPagedWarps], M = -INFINITY, L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPagedWarps; ++i) {
+            e[i] = mls[i * kPagedRows + r0 + r];
+            x[i] = obuf[(i * OR + r) * kPagedMergeCols + 4 * paged_piece(col >> 2, r) + (col & 3)];
+            M = fmaxf(M, e[i].x);
+        }
         const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int i = 0; i < kPagedWarps; ++i) {
-            const float2 e = mls[i * kPagedRows + r0 + r];
-            const float f = exp2f(e.x - base);
-            L = fmaf(f, e.y, L);
-            acc = fmaf(f, obuf[(i * OR + r) * DV + col], acc);
+            const float f = ex2(e[i].x - base);
+            L = fmaf(f, e[i].y, L);
+            acc = fmaf(f, x[i], acc);
         }
         if (whole) {
             const bool none = L == 0.f;   // nothing to attend to
-            if (col < p.c.dv) st((T *)p.y + (hq0 + r0 + r) * p.c.dv + col, none ? 0.f : acc / L);
-            if (col == 0) {
+            if (col0 + col < p.c.dv) st((T *)p.y + (hq0 + r0 + r) * p.c.dv + col0 + col, none ? 0.f : acc / L);
+            if (col0 + col == 0) {
                 if (p.lse) p.lse[hq0 + r0 + r] = none ? -INFINITY : M * 0.693147180559945309f + logf(L);
                 if (p.lse2) p.lse2[hq0 + r0 + r] = none ? -INFINITY : M + log2f(L);
             }
         } else {
             const size_t at = ((size_t)blockIdx.x * 2 + slot) * kPagedRows + r0 + r;
-            if (col < p.c.dv) p.part[at * p.c.dv + col] = acc;
-            if (col == 0) p.ml[at] = make_float2(M, L);
+            if (col0 + col < p.c.dv) p.part[at * p.c.dv + col0 + col] = acc;
+            if (col0 + col == 0) p.ml[at] = make_float2(M, L);
         }
     }
 }
@@ -359,14 +383,6 @@ __device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const
     }
     const int off = c.shift >= 0 ? t & (c.page - 1) : t % c.page;
     return (entry * c.Hkv + w.h) * c.page + off;
-}
-
-// 2^x; results below 2^-126 are 0.
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
@@ -584,6 +600,16 @@ struct PagedFeed {
         if (TMA) sm100::fence_proxy_async();   // before a later copy writes this place
         __syncwarp();
     }
+    // Masked slots have no weight, but their rows of a place may hold anything,
+    // and 0 * NaN is NaN: zeros.
+    __device__ __forceinline__ void clear(uint8_t *dst, int blocks, uint32_t mask)
+    {
+        if (lane < SLOTS && !(mask >> lane & 1))
+            for (int i = 0; i < blocks * 8; ++i)
+                *reinterpret_cast<uint4 *>(dst + (i >> 3) * BLOCK + lane * 128 + (((i ^ lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        if (TMA) sm100::fence_proxy_async();   // before a later copy writes this place
+        __syncwarp();
+    }
     __device__ __forceinline__ PagedTile tile(int it) const
     {
         const int4 *from = reinterpret_cast<const int4 *>(tiles_at + it % kPagedAhead);
@@ -661,7 +687,7 @@ struct PagedMma {
     using Feed = PagedFeed<__nv_bfloat16, __nv_bfloat16, KB, VB, 32, ST, true>;
     static constexpr int BLOCK = Feed::BLOCK;
     static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
-    static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * DV * 4;
+    static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * kPagedMergeCols * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
     static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * (int)sizeof(PagedTile);
     static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
@@ -746,16 +772,8 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         float *const sc = p.scores ? p.scores + (w.hq(p) + r) * p.stride + (w.tile << 7) + warp * 32 : nullptr;
         uint8_t *kp = feed.take(t.copies);
         feed.issue();   // into the place before, which every lane has used; with it the next tile is known
-        // the next unit's queries are on their way while this one is finished
-        auto next_q = [&]() {
-            if (it + 1 >= tiles || w.tile != w.nt - 1) return;
-            __syncwarp();
-            load_q(paged_unit(p, feed.tile(it + 1)));
-        };
-
-        // one tile; `whole`: every slot is attended to
-        auto work = [&](auto whole_tag) {
-            constexpr bool WHOLE = decltype(whole_tag)::value;
+        uint32_t hi[4][NR], lo[4][NR];   // P: [slots 8 i + sv.][row]
+        if (mask && feed.alive) {
             if (t.newrow >= 0) feed.patch(kp, (const T *)p.k + w.bh(p) * c.dqk, (T *)c.kp, c.dqk, Cfg::KB, t);
             const uint32_t ks = smem_addr(kp);
             float s[4][4];
@@ -772,7 +790,6 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mma_16816(s[i], a.z, b.z, a.w, b.w, kk[i].z, kk[i].w);
             }
-            next_q();
             // scores in log2 units; slot of s[i][e] (and s[i][e + 2]): 8 i + sv_e
             float mn[NR];
 #pragma unroll
@@ -783,8 +800,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float &x = s[i][n * 2 + e];
-                        x *= p.scale_log2;
-                        if (!WHOLE && !(mask >> (8 * i + (e ? sv1 : sv0)) & 1)) x = -INFINITY;
+                        x = mask >> (8 * i + (e ? sv1 : sv0)) & 1 ? x * p.scale_log2 : -INFINITY;
                         mn[n] = fmaxf(mn[n], x);
                     }
                 mn[n] = fmaxf(mn[n], __shfl_xor_sync(ALL, mn[n], 1));
@@ -815,7 +831,6 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                     o[i][3] *= al[NR - 1];
                 }
             }
-            uint32_t hi[4][NR], lo[4][NR];   // [slots 8 i + sv.][row]
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float base = m[n] == -INFINITY ? 0.f : m[n];
@@ -829,10 +844,24 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 }
                 l[n] += sum;
             }
-            uint8_t *vp = feed.take(t.copies);
-            feed.issue();
-            if (!feed.alive) return;
+        } else if (sc && w.n > 0) {   // slots past the end, or on bad pages: no weight
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                if (r + 8 * n < rows)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[8 * n * p.stride + 8 * i + sv0] = sc[8 * n * p.stride + 8 * i + sv1] = -INFINITY;
+        }
+        // the next unit's queries are on their way while this one is finished
+        if (it + 1 < tiles && w.tile == w.nt - 1) {
+            __syncwarp();
+            load_q(paged_unit(p, feed.tile(it + 1)));
+        }
+        uint8_t *vp = feed.take(t.copies);
+        feed.issue();
+        if (mask && feed.alive) {
             if (t.newrow >= 0) feed.patch(vp, (const T *)p.v + w.bh(p) * c.dv, (T *)c.vp, c.dv, Cfg::VB, t);
+            if (mask != ALL) feed.clear(vp, Cfg::VB, mask);
             const uint32_t vs = smem_addr(vp);
 #pragma unroll
             for (int j = 0; j < DV / 64; ++j) {
@@ -841,12 +870,8 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 for (int kk = 0; kk < 2; ++kk) {
                     uint4 vv[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 4; ++i)
                         vv[i] = lds128(vs + (i & 1 ? off_v1 : off_v0) + (2 * kk + (i >> 1)) * 1024 + j * Cfg::BLOCK);
-                        // a masked slot's weight is 0, but its row may hold anything: 0 * NaN is NaN
-                        if (!WHOLE && !(mask >> ((2 * kk + (i >> 1)) * 8 + (i & 1 ? sv1 : sv0)) & 1))
-                            vv[i] = make_uint4(0u, 0u, 0u, 0u);
-                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
@@ -862,22 +887,6 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                     }
                 }
             }
-        };
-        if (mask == ALL && feed.alive) {
-            work(std::true_type{});
-        } else if (mask && feed.alive) {
-            work(std::false_type{});
-        } else {   // slots past the end, or on bad pages: no weight
-            if (sc && w.n > 0)
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-                    if (r + 8 * n < rows)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sc[8 * n * p.stride + 8 * i + sv0] = sc[8 * n * p.stride + 8 * i + sv1] = -INFINITY;
-            next_q();
-            feed.take(false);
-            feed.issue();
         }
         if (w.tile == w.nt - 1 || it == tiles - 1) {   // the unit, or its part in this range, ends
             bool whole;
@@ -892,26 +901,27 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                     if (cq == 0) mls[warp * kPagedRows + r + 8 * n] = make_float2(m[n], l[n]);
                 }
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float4 *to = reinterpret_cast<float4 *>(obuf + (warp * 8 + r) * DV + cq * 16);
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int j = 0; j < DV / 64; ++j)
+                    for (int j = 0; j < DV / 64; ++j) {
+                        float4 *to = reinterpret_cast<float4 *>(obuf + (warp * 8 + r) * kPagedMergeCols);
+                        if (r + 8 * n < rows)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int f = 0; f < 2; ++f) {
-                                float x[4];
+                                for (int f = 0; f < 2; ++f) {
+                                    float x[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float *oo = o[j * 8 + f * 4 + i];
-                                    x[i] = HI ? oo[n * 2 + e] : oo[e] + oo[e + 2];
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float *oo = o[j * 8 + f * 4 + i];
+                                        x[i] = HI ? oo[n * 2 + e] : oo[e] + oo[e + 2];
+                                    }
+                                    to[paged_piece(cq * 4 + e * 2 + f, r)] = make_float4(x[0], x[1], x[2], x[3]);
                                 }
-                                to[j * 16 + e * 2 + f] = make_float4(x[0], x[1], x[2], x[3]);
-                            }
-                    __syncthreads();
-                    paged_merge<T, DV, 8>(p, w, obuf, mls, 8 * n, rows, whole, slot);
-                    __syncthreads();
-                }
+                        __syncthreads();
+                        paged_merge<T, 8>(p, w, obuf, mls, 8 * n, 64 * j, rows, whole, slot);
+                        __syncthreads();
+                    }
                 paged_store_position(p, w);
             }
         }
@@ -932,7 +942,7 @@ struct PagedSimt {
     static constexpr int BLOCK = Feed::BLOCK;
     static constexpr int LR = D / 4, TP = 32 / LR;   // lanes per value row, rows per pass
     static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
-    static constexpr int OFF_Q = OFF_O + kPagedWarps * OR * D * 4;         // [GM][D] queries, shared by the warps
+    static constexpr int OFF_Q = OFF_O + kPagedWarps * OR * kPagedMergeCols * 4;   // [GM][D] queries, shared by the warps
     static constexpr int OFF_P = OFF_Q + GM * D * 4;                       // [warp][16][GM] weights
     static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
@@ -1069,13 +1079,12 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
             feed.issue();
             if (t.newrow >= 0 && feed.alive) feed.patch(vp, (const T *)p.v + w.bh(p) * c.dv, (T *)c.vp, c.dv, Cfg::NB, t);
             const uint32_t vs = smem_addr(vp) + off_v;
-            if (feed.alive)
+            if (feed.alive) {
+                if (mask != 0xffffu) feed.clear(vp, Cfg::NB, mask);
 #pragma unroll
                 for (int i = 0; i < 16 / Cfg::TP; ++i) {
                     const int row = i * Cfg::TP + vrow;
-                    float4 x = lds_f4(vs + row * 128 + (((lane ^ row) & 7) << 4));
-                    // a masked slot's weight is 0, but its row may hold anything: 0 * NaN is NaN
-                    if (!(mask >> row & 1)) x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 x = lds_f4(vs + row * 128 + (((lane ^ row) & 7) << 4));
                     const float *pp = ps + row * GM;
 #pragma unroll
                     for (int n = 0; n < GM; ++n) {
@@ -1087,6 +1096,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                         o[n].w = fmaf(f, x.w, o[n].w);
                     }
                 }
+            }
             __syncwarp();   // the weights are read before the next tile's
         } else {
             if (p.scores && w.n > 0 && cq == 0)
@@ -1115,14 +1125,18 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                     if (lane == 0) mls[warp * kPagedRows + n] = make_float2(m[n], l[n]);
                 }
 #pragma unroll
-                for (int n0 = 0; n0 < GM; n0 += 8) {
+                for (int n0 = 0; n0 < GM; n0 += 8)
 #pragma unroll
-                    for (int n = n0; n < GM && n < n0 + 8; ++n)
-                        if (vrow == 0) *reinterpret_cast<float4 *>(obuf + (warp * Cfg::OR + n - n0) * D + vcol) = o[n];
-                    __syncthreads();
-                    paged_merge<T, D, Cfg::OR>(p, w, obuf, mls, n0, min(rows, GM), whole, slot);
-                    __syncthreads();
-                }
+                    for (int c0 = 0; c0 < D; c0 += kPagedMergeCols) {
+#pragma unroll
+                        for (int n = n0; n < GM && n < n0 + 8; ++n)
+                            if (vrow == 0 && vcol >= c0 && vcol < c0 + kPagedMergeCols)
+                                *reinterpret_cast<float4 *>(obuf + (warp * Cfg::OR + n - n0) * kPagedMergeCols +
+                                                            4 * paged_piece((vcol - c0) >> 2, n - n0)) = o[n];
+                        __syncthreads();
+                        paged_merge<T, Cfg::OR>(p, w, obuf, mls, n0, c0, min(rows, GM), whole, slot);
+                        __syncthreads();
+                    }
                 paged_store_position(p, w);
             }
         }
@@ -1141,12 +1155,12 @@ __device__ __forceinline__ float2 paged_part_ml(const PagedDecodeParams &p, int 
 // lanes share one output's parts (as many as leave one output to each group, so
 // that the loads of a lane, one after the other, are few).
 template <typename T>
-__device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const PagedSpan &s, long long chunk)
+__device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const PagedSpan &s, long long chunk, int range)
 {
     const int g0 = (int)(s.first / chunk), g1 = (int)((s.end - 1) / chunk), K = g1 - g0 + 1, dv = p.c.dv;
     const int h = s.u / p.nsub, sub = s.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
     const size_t hq0 = (size_t)s.b * p.Hq + h * p.g + sub * p.gs;
-    const int E = rows * dv, per = (E + K - 1) / K, e0 = (blockIdx.x - g0) * per, e1 = min(E, e0 + per);
+    const int E = rows * dv, per = (E + K - 1) / K, e0 = (range - g0) * per, e1 = min(E, e0 + per);
     int KL = 1;
     while (KL < K && KL < 32 && per * KL * 2 <= kPagedJoinThreads) KL <<= 1;
     const int mine = threadIdx.x & (KL - 1);
@@ -1198,17 +1212,26 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
     }
 }
 
-template <typename T>
+// One block per range, or with weights kPagedWeightBlocks of them: the first one
+// joins, and each adds the weights of its part of the range's tiles.
+template <typename T, bool WEIGHTS>
 __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const PagedDecodeParams p)
 {
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
+    const int range = WEIGHTS ? blockIdx.x / kPagedWeightBlocks : blockIdx.x;
+    const int share = WEIGHTS ? blockIdx.x % kPagedWeightBlocks : 0;
+    const PagedRecord &rec = p.rec[range];
+    const int tiles = rec.tiles;
+    if (!tiles) return;
+    const long long per_range = rec.chunk;
+    if (share == 0) {
+        const PagedSpan head = rec.head, tail = rec.tail;
+        if (head.b >= 0) paged_join<T>(p, head, per_range, range);
+        if (tail.b >= 0) paged_join<T>(p, tail, per_range, range);
+    }
+    if constexpr (!WEIGHTS) return;
     __shared__ float lse2[kPagedMaxGroup];
-    const PagedRecord rec = p.rec[blockIdx.x];
-    if (!rec.tiles) return;
-    if (rec.head.b >= 0) paged_join<T>(p, rec.head, rec.chunk);
-    if (rec.tail.b >= 0) paged_join<T>(p, rec.tail, rec.chunk);
-    if (!p.w_out) return;
     // weights of the range's slots, each head's first unit for all its units
     const PagedCache &c = p.c;
     const int tid = threadIdx.x;
@@ -1218,8 +1241,18 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
     w.sub = rec.u - w.h * p.nsub;
     w.tile = rec.tile;
     w.set(p, paged_count(p, w.b));
-    long long at = blockIdx.x * rec.chunk;
-    for (int left = rec.tiles; left > 0;) {
+    auto count = [&](int b) { return paged_count(p, b); };
+    // this block's tiles of the range
+    const int from = (int)((long long)tiles * share / kPagedWeightBlocks);
+    int left = (int)((long long)tiles * (share + 1) / kPagedWeightBlocks) - from;
+    for (int skip = from; skip > 0;) {
+        const int here = min(skip, w.nt - w.tile);
+        w.tile += here - 1;
+        w.next(p, count);
+        skip -= here;
+    }
+    long long at = range * per_range + from;
+    while (left > 0) {
         const int here = min(left, w.nt - w.tile);
         if (w.sub == 0 && w.n > 0) {
             const size_t hq0 = w.hq(p), bh = w.bh(p);
@@ -1227,7 +1260,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
             for (int j = tid; j < p.g; j += kPagedJoinThreads) {
                 const int sub = j / p.gs;
                 const long long first = at - w.tile + (long long)sub * w.nt;   // of this head's unit
-                const int g0 = (int)(first / rec.chunk), g1 = (int)((first + w.nt - 1) / rec.chunk);
+                const int g0 = (int)(first / per_range), g1 = (int)((first + w.nt - 1) / per_range);
                 if (g0 == g1) {
                     lse2[j] = p.lse2[hq0 + j];
                 } else {
@@ -1274,7 +1307,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
         at += here;
         if (left > 0) {
             w.tile += here - 1;
-            w.next(p, [&](int b) { return paged_count(p, b); });
+            w.next(p, count);
         }
     }
 }
