@@ -1380,7 +1380,7 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
                          : dtype == LA_F32  ? paged_simt<float, false>(p, pl, st)
                                             : paged_simt<__nv_bfloat16, false>(p, pl, st);
     if (s1 != LA_OK || pl.aligned) return s1;
-    const int jg = weights_in ? pl.grid * kPagedWeightBlocks : pl.grid;
+    const int jg = weights_in ? pl.grid * (kPagedWeightBlocks + 1) : pl.grid;
     if (dtype == LA_F32)
         return weights_in ? launch_pdl(paged_join_kernel<float, true>, jg, kPagedJoinThreads, 0, st, p)
                           : launch_pdl(paged_join_kernel<float, false>, jg, kPagedJoinThreads, 0, st, p);

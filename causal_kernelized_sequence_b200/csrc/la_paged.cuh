@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
 constexpr int kPagedJoinThreads = 128;     // of the join
-constexpr int kPagedWeightBlocks = 4;      // with weights: blocks of the join per range
+constexpr int kPagedWeightBlocks = 3;      // more blocks of it per range where weights are kept (all run at once)
 constexpr int kPagedRows = 16;       // query heads of a unit
 constexpr int kPagedMaxGroup = 128;  // query heads per key/value head
 
@@ -1144,6 +1144,12 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
     feed.drain();
 }
 
+// a / b of non-negative numbers (a 32-bit division is a fraction of a 64-bit one)
+__device__ __forceinline__ int paged_div(long long a, long long b)
+{
+    return (int)(a <= INT_MAX && b <= INT_MAX ? (unsigned)a / (unsigned)b : a / b);
+}
+
 // Maximum and sum of row `row` over the parts of a unit that crosses ranges.
 __device__ __forceinline__ float2 paged_part_ml(const PagedDecodeParams &p, int g0, int i, int row)
 {
@@ -1157,7 +1163,7 @@ __device__ __forceinline__ float2 paged_part_ml(const PagedDecodeParams &p, int 
 template <typename T>
 __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const PagedSpan &s, long long chunk, int range)
 {
-    const int g0 = (int)(s.first / chunk), g1 = (int)((s.end - 1) / chunk), K = g1 - g0 + 1, dv = p.c.dv;
+    const int g0 = paged_div(s.first, chunk), g1 = paged_div(s.end - 1, chunk), K = g1 - g0 + 1, dv = p.c.dv;
     const int h = s.u / p.nsub, sub = s.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
     const size_t hq0 = (size_t)s.b * p.Hq + h * p.g + sub * p.gs;
     const int E = rows * dv, per = (E + K - 1) / K, e0 = (range - g0) * per, e1 = min(E, e0 + per);
@@ -1212,23 +1218,24 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
     }
 }
 
-// One block per range, or with weights kPagedWeightBlocks of them: the first one
-// joins, and each adds the weights of its part of the range's tiles.
+// One block per range joins; with weights kPagedWeightBlocks more add the
+// weights of a part of the range's tiles each.
 template <typename T, bool WEIGHTS>
-__global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const PagedDecodeParams p)
+__global__ void __launch_bounds__(kPagedJoinThreads, 8) paged_join_kernel(const PagedDecodeParams p)
 {
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
-    const int range = WEIGHTS ? blockIdx.x / kPagedWeightBlocks : blockIdx.x;
-    const int share = WEIGHTS ? blockIdx.x % kPagedWeightBlocks : 0;
+    constexpr int PER = WEIGHTS ? kPagedWeightBlocks + 1 : 1;
+    const int range = blockIdx.x / PER, share = blockIdx.x % PER;
     const PagedRecord &rec = p.rec[range];
     const int tiles = rec.tiles;
     if (!tiles) return;
     const long long per_range = rec.chunk;
-    if (share == 0) {
+    if (share == PER - 1) {
         const PagedSpan head = rec.head, tail = rec.tail;
         if (head.b >= 0) paged_join<T>(p, head, per_range, range);
         if (tail.b >= 0) paged_join<T>(p, tail, per_range, range);
+        return;
     }
     if constexpr (!WEIGHTS) return;
     __shared__ float lse2[kPagedMaxGroup];
@@ -1260,9 +1267,10 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
             for (int j = tid; j < p.g; j += kPagedJoinThreads) {
                 const int sub = j / p.gs;
                 const long long first = at - w.tile + (long long)sub * w.nt;   // of this head's unit
-                const int g0 = (int)(first / per_range), g1 = (int)((first + w.nt - 1) / per_range);
+                const int g0 = paged_div(first, per_range), g1 = paged_div(first + w.nt - 1, per_range);
                 if (g0 == g1) {
-                    lse2[j] = p.lse2[hq0 + j];
+                    const float x = p.lse2[hq0 + j];
+                    lse2[j] = x == -INFINITY ? INFINITY : x;   // nothing attended to: 2^(s - inf) = 0
                 } else {
                     float M = -INFINITY, L = 0.f;
 #pragma unroll 8
@@ -1272,7 +1280,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
                         const float2 e = paged_part_ml(p, g0, i, j - sub * p.gs);
                         L = fmaf(ex2(e.x - (M == -INFINITY ? 0.f : M)), e.y, L);
                     }
-                    lse2[j] = L == 0.f ? -INFINITY : M + log2f(L);
+                    lse2[j] = L == 0.f ? INFINITY : M + log2f(L);
                 }
             }
             __syncthreads();
@@ -1280,27 +1288,38 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_join_kernel(const Pag
             const int end = min((long long)w.n, (long long)(w.tile + here) << p.tile);
             const float *wi = p.w_in + bh * c.cap();
             float *wo = p.w_out + bh * c.cap();
+            const bool vec = ((reinterpret_cast<uintptr_t>(wi) | reinterpret_cast<uintptr_t>(wo)) & 15) == 0;
+            const int fresh = p.k ? w.n - 1 : -1;
             for (int t = (w.tile << p.tile) + 4 * tid; t < end; t += 4 * kPagedJoinThreads) {
-                float sum[4], old[4];
+                __align__(16) float sum[4], old[4];
+                const bool four = vec && t + 4 <= end;
+                if (four) {
+                    *reinterpret_cast<float4 *>(old) = *reinterpret_cast<const float4 *>(wi + t);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    old[e] = t + e < end && !(p.k && t + e == w.n - 1) ? wi[t + e] : 0.f;
-                    sum[e] = 0.f;
+                    for (int e = 0; e < 4; ++e) old[e] = t + e < end ? wi[t + e] : 0.f;
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = 0.f;
+                const float *sc = p.scores + hq0 * p.stride + t;
 #pragma unroll 4
-                for (int j = 0; j < p.g; ++j) {
-                    const float4 s = *reinterpret_cast<const float4 *>(p.scores + (hq0 + j) * p.stride + t);
+                for (int j = 0; j < p.g; ++j, sc += p.stride) {
+                    const float4 s = *reinterpret_cast<const float4 *>(sc);
                     const float L = lse2[j];
-                    if (L != -INFINITY) {
-                        sum[0] += ex2(s.x - L);
-                        sum[1] += ex2(s.y - L);
-                        sum[2] += ex2(s.z - L);
-                        sum[3] += ex2(s.w - L);
-                    }
+                    sum[0] += ex2(s.x - L);
+                    sum[1] += ex2(s.y - L);
+                    sum[2] += ex2(s.z - L);
+                    sum[3] += ex2(s.w - L);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t + e < end) wo[t + e] = old[e] + sum[e];
+                for (int e = 0; e < 4; ++e) old[e] = (t + e == fresh ? 0.f : old[e]) + sum[e];
+                if (four) {
+                    *reinterpret_cast<float4 *>(wo + t) = *reinterpret_cast<const float4 *>(old);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t + e < end) wo[t + e] = old[e];
+                }
             }
         }
         left -= here;
