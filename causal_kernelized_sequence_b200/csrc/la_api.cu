@@ -1302,11 +1302,9 @@ la_status la_paged_cache_fill(const void *k, const void *v, void *k_pages, void 
     p.weights = weights;
     p.positions = positions;
     p.N = N;
-    p.vec_k = rows16(dqk, dtype);
-    p.vec_v = rows16(dv, dtype);
-    cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == LA_F32) return launch_pdl(paged_fill_kernel<float>, (int)blocks, kPagedFillThreads, 0, st, p);
-    return launch_pdl(paged_fill_kernel<__nv_bfloat16>, (int)blocks, kPagedFillThreads, 0, st, p);
+    p.elem = (int)elem_size(dtype);
+    p.width = rows16(dqk, dtype) && rows16(dv, dtype) ? 16 : p.elem;
+    return launch_pdl(paged_fill_kernel, (int)blocks, kPagedFillThreads, 0, (cudaStream_t)stream, p);
 }
 
 size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,

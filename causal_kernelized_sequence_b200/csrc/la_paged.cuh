@@ -31,19 +31,6 @@ __device__ __forceinline__ int paged_row(const PagedCache &c, int b, int h, int 
     return (pg * c.Hkv + h) * c.page + (t - i * c.page);
 }
 
-// 16-byte copies where every row starts on a 16-byte boundary, elements otherwise.
-template <typename T, int LANES>
-__device__ __forceinline__ void copy_row(T *dst, const T *src, int d, bool vec, int lane)
-{
-    if (vec) {
-        constexpr int E = 16 / sizeof(T);
-        for (int i = lane; i < d / E; i += LANES)
-            reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(src)[i];
-    } else {
-        for (int i = lane; i < d; i += LANES) dst[i] = src[i];
-    }
-}
-
 // ------------------------------------------------------------------ append
 
 constexpr int kPagedFillThreads = 256;
@@ -56,11 +43,46 @@ struct PagedFillParams {
     float *weights;
     int *positions;
     int N;
-    bool vec_k, vec_v;
+    int elem;    // bytes of an element
+    int width;   // bytes a copy moves at once: 16 if both rows allow it, else an element
 };
 
+// Rows `src` + i of k and v to rows[i] of the pool, for this warp's eight of the
+// block's 64: a power of two of lanes copies a row pair, eight pairs in flight.
+template <typename V>
+__device__ __forceinline__ void fill_rows(const PagedFillParams &p, size_t src, const int *rows, int m)
+{
+    constexpr int U = 8;
+    const PagedCache &c = p.c;
+    const int pk = c.dqk * p.elem / (int)sizeof(V), pv = c.dv * p.elem / (int)sizeof(V), np = pk + pv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int per_row = 1;
+    while (per_row < np && per_row < 32) per_row <<= 1;
+    const int groups = 32 / per_row, sub = lane / per_row, piece0 = lane & (per_row - 1);
+    const V *k = (const V *)p.k + src * pk, *v = (const V *)p.v + src * pv;
+    V *kp = (V *)c.kp, *vp = (V *)c.vp;
+    constexpr int WARPS = kPagedFillThreads / 32;
+    for (int i0 = warp * U * groups; i0 < m; i0 += WARPS * U * groups)
+        for (int q = piece0; q < np; q += per_row) {
+            const bool isk = q < pk;
+            const V *from = isk ? k + q : v + (q - pk);
+            V *to = isk ? kp + q : vp + (q - pk);
+            const size_t stride = isk ? pk : pv;
+            V x[U];
+            int row[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * groups + sub;
+                row[u] = i < m ? rows[i] : -1;
+                if (row[u] >= 0) x[u] = from[i * stride];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (row[u] >= 0) to[row[u] * stride] = x[u];
+        }
+}
+
 // One block per 64 new tokens of a (b, h): slot lens[b] + i <- token i.
-template <typename T>
 __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const PagedFillParams p)
 {
     sm100::grid_dependency_wait();
@@ -68,9 +90,8 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
     __shared__ int rows[kPagedFillRows];
     const PagedCache &c = p.c;
     const int tiles = (p.N + kPagedFillRows - 1) / kPagedFillRows;
-    const long long bh = blockIdx.x / tiles;
-    const int i0 = (int)(blockIdx.x - bh * tiles) * kPagedFillRows;
-    const int b = (int)(bh / c.Hkv), h = (int)(bh - (long long)b * c.Hkv);
+    const int bh = blockIdx.x / tiles, i0 = (blockIdx.x - bh * tiles) * kPagedFillRows;
+    const int b = bh / c.Hkv, h = bh - b * c.Hkv;
     const int tid = threadIdx.x;
     const int len = c.lens[b], n = p.n_new ? p.n_new[b] : p.N, pos = p.pos ? p.pos[b] : 0;
     if (len < 0 || n < 0 || n > p.N || (long long)len + n > c.cap() || pos < 0) {
@@ -90,15 +111,10 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
         if (p.positions) p.positions[bh * c.cap() + t] = pos + i0 + i;
     }
     __syncthreads();
-    constexpr int G = 8;   // threads per row
-    const int lane = tid % G;
-    for (int i = tid / G; i < m; i += kPagedFillThreads / G) {
-        const int row = rows[i];
-        if (row < 0) continue;
-        const size_t src = bh * (size_t)p.N + i0 + i;
-        copy_row<T, G>((T *)c.kp + (size_t)row * c.dqk, (const T *)p.k + src * c.dqk, c.dqk, p.vec_k, lane);
-        copy_row<T, G>((T *)c.vp + (size_t)row * c.dv, (const T *)p.v + src * c.dv, c.dv, p.vec_v, lane);
-    }
+    const size_t src = bh * (size_t)p.N + i0;
+    if (p.width == 16) fill_rows<uint4>(p, src, rows, m);
+    else if (p.width == 4) fill_rows<uint32_t>(p, src, rows, m);
+    else fill_rows<uint16_t>(p, src, rows, m);
 }
 
 // ------------------------------------------------------- one-token attention
@@ -1363,9 +1379,9 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Copies the moved rows of this block's share of the list.  A warp takes up to
-// 32 moves, one lane looks up each of them, and then a power of two of lanes
-// copies each row pair, U pairs in flight.
+// Moves this block's share of the list.  A warp takes up to 32 moves, one lane
+// looks up each of them and moves its weight and position, and then a power of
+// two of lanes copies each row pair, U pairs in flight.
 template <typename V, int U>
 __device__ __forceinline__ void evict_rows(const PagedEvictParams &p, int b, int h, const int *holes,
                                            const int *movers, int m, int rank, int blocks)
@@ -1383,8 +1399,12 @@ __device__ __forceinline__ void evict_rows(const PagedEvictParams &p, int b, int
         const int cnt = min(share, m - i0);
         int to = 0, from = 0;
         if (lane < cnt) {
-            to = paged_row(c, b, h, holes[i0 + lane]);
-            from = paged_row(c, b, h, movers[i0 + lane]);
+            const int hole = holes[i0 + lane], mover = movers[i0 + lane];
+            to = paged_row(c, b, h, hole);
+            from = paged_row(c, b, h, mover);
+            const size_t base = ((size_t)b * c.Hkv + h) * c.cap();
+            p.w_out[base + hole] = p.w_in[base + mover];
+            if (p.pos_out) p.pos_out[base + hole] = p.pos_in[base + mover];
         }
         for (int i = 0; i < cnt; i += U * groups) {
             int rt[U], rf[U];
@@ -1514,26 +1534,6 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
         }
     };
 
-    // the table's entries; a bad one leaves the sequence as it was
-    for (int i = tid; i < 2 * BINS / 4; i += kEvictThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
-    bool bad = false;
-    const int used = (n - 1) / c.page + 1;
-#pragma unroll 4
-    for (int i = rank * kEvictThreads + tid; i < used; i += CS * kEvictThreads)
-        bad |= (unsigned)c.table[(size_t)b * c.max_pages + i] >= (unsigned)c.num_pages;
-    int bads = __syncthreads_or(bad), none;
-    if constexpr (CLUSTER) {
-        if (tid == 0) xch[0] = bads != 0;
-        sync_all();
-        bads = gather(0, none);
-    }
-    if (bads) {
-        if (rank == 0 && tid == 0) report(kStatusCheck);
-        if (first && p.newlen) len_to[b] = n;
-        sync_all();   // no block leaves while another reads its xch
-        return;
-    }
-
     // f(t0, key, in) for this warp's slots, 32 at a time from t0 on (slot t0 + lane,
     // `in` if it exists), their keys loaded four times 32 at once
     auto sweep = [&](auto f) {
@@ -1546,14 +1546,15 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
                 if (t + 32 * j < a1) f(t + 32 * j, key[j], t + 32 * j + lane < a1);
         }
     };
-    // the keys, the number of recent tokens, and the entries of slots that may
-    // stay (those of dropped ones are written again below)
-    int late = 0;
-    for (int t = a0 + lane; t < a1; t += 128) {
-        float x[4];
-        int y[4];
+    // the keys, the number of recent tokens, and the table's entries
+    for (int i = tid; i < 2 * BINS / 4; i += kEvictThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
+    constexpr int KU = 6;   // loads in flight per lane
+    int late = 0, none;
+    for (int t = a0 + lane; t < a1; t += 32 * KU) {
+        float x[KU];
+        int y[KU];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KU; ++j) {
             x[j] = 0.f;
             y[j] = 0;
             if (t + 32 * j < a1) {
@@ -1562,29 +1563,43 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KU; ++j) {
             const int at = t + 32 * j;
             if (at >= a1) break;
             const bool l = p.recent && y[j] >= last - p.recent;
             late += l;
             if (cached) keys[at - s0] = l ? 0xffffffffu : weight_key(x[j]);
-            if (at < budget) {
+            if (at < budget) {   // other buffers: entries that may stay (those of dropped slots are written again below)
                 if (wo != w) wo[at] = x[j];
                 if (po != ps) po[at] = y[j];
             }
         }
     }
+    bool bad = false;
+    const int used = (n - 1) / c.page + 1;
+#pragma unroll 4
+    for (int i = rank * kEvictThreads + tid; i < used; i += CS * kEvictThreads)
+        bad |= (unsigned)c.table[(size_t)b * c.max_pages + i] >= (unsigned)c.num_pages;
     int total;
     (void)warps_before(__reduce_add_sync(0xffffffffu, late), part[0], total);
-    if (tid == 0) xch[1] = total;
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        xch[0] = bad;
+        xch[1] = total;
+    }
     sync_all();
+    if (gather(0, none)) {   // a bad entry: the sequence stays as it was
+        if (rank == 0 && tid == 0) report(kStatusCheck);
+        if (first && p.newlen) len_to[b] = n;
+        sync_all();   // no block leaves while another reads its xch
+        return;
+    }
     if (gather(1, none) > budget) {
         crowded = true;
         if (cached)
             for (int t = a0 + lane; t < a1; t += 32) keys[t - s0] = make_key(t);
         __syncthreads();
     }
-
     // the radix select, from the top; it ends early when a whole bin stays.  Kept
     // are the keys whose `known` bits are above thr, and `need` of the `ties`
     // slots where they are thr.
@@ -1734,11 +1749,6 @@ __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(cons
         im += __shfl_sync(0xffffffffu, sm, 31);
     }
     sync_all();   // the lists are complete, all keys are read, and no block reads another's memory any more
-    for (int i = rank * kEvictThreads + tid; i < m; i += CS * kEvictThreads) {
-        const int to = holes[i], from = movers[i];
-        wo[to] = w[from];
-        if (po) po[to] = ps[from];
-    }
     if (first) len_to[b] = budget;
     if (p.width == 16) evict_rows<uint4, U>(p, b, h, holes, movers, m, rank, CS);
     else if (p.width == 4) evict_rows<uint32_t, U>(p, b, h, holes, movers, m, rank, CS);

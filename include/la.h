@@ -354,7 +354,8 @@ LA_API la_status la_swa_decode_step(const void *q, const void *k, const void *v,
  * as it was (its outputs are not written either) and sets LA_ERR_DEVICE_CHECK
  * in the device status word.  A block_table entry outside [0, num_pages) sets
  * it too; its tokens are neither written nor, in a decode step, attended to,
- * and la_paged_evict leaves the sequence as it was. */
+ * and la_paged_evict leaves the sequence as it was (what it writes to outputs
+ * that are not its inputs is then undefined). */
 
 /* Append tokens to the cache: slot lens[b] + i takes k[b,h,i], v[b,h,i] for
  * i < n_new[b].  The counterpart of la_swa_cache_fill: k, v [B,Hkv,N,*] dtype
