@@ -121,10 +121,13 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 //
 // For every sequence b and key/value head h, up to 16 query heads that share
 // the head form a unit (groups of more than 16 heads are several units), and a
-// unit's slots are cut into tiles of 64.  All tiles of the call, in (b, h, tile)
-// order, are dealt out in equal contiguous ranges, one per block: one long
-// sequence or many ragged ones load every SM alike, and each block finds its
-// range from lens by one scan.  Inside a tile each of the four warps owns a quarter
+// unit's slots are cut into tiles of 64 or 128.  All tiles of the call, in
+// (b, h, tile) order, are dealt out in contiguous ranges of equal cost, one per
+// block: one long sequence or many ragged ones load every SM alike, and each
+// block finds its range from lens by one scan.  A tile counts 4 and the end of a
+// unit 3, as they take (1.7 and 1.3 us at d = 64 with three blocks on an SM); a
+// tile belongs to the range in which its cost begins.
+// Inside a tile each of the four warps owns a quarter
 // of the slots, with its own running maximum, sum and accumulators, so warps meet only
 // where a unit ends.  A unit inside one range is finished there; the parts of
 // one that crosses ranges go to the workspace and the join kernel adds them,
@@ -140,17 +143,20 @@ constexpr int kPagedWeightBlocks = 3;      // more blocks of it per range where 
 constexpr int kPagedRows = 16;       // query heads of a unit
 constexpr int kPagedMaxGroup = 128;  // query heads per key/value head
 
-// A unit that crosses ranges, as the join needs it: tiles [first, end) of all.
+constexpr int kTileCost = 4, kUnitCost = 3;
+
+// A unit that crosses ranges, as the join needs it: its tiles' costs begin at
+// first, first + kTileCost, ..
 struct PagedSpan {
-    long long first, end;
-    int b, u;   // b < 0: none
+    long long first;
+    int nt, b, u;   // b < 0: none
 };
 // What a block of the decode kernel leaves for the block of the join: where
 // its range starts, and the units it shares with the ranges before and after.
 struct PagedRecord {
     PagedSpan head, tail;
-    int b, u, tile, tiles;   // start of the range, and its length (0: idle)
-    long long chunk;         // tiles per range
+    int b, u, tile, tiles;   // start of the range, and its length in tiles (0: idle)
+    long long at, chunk;     // where the first tile's cost begins, and the cost of a range
 };
 
 struct PagedDecodeParams {
@@ -244,40 +250,49 @@ struct PagedWalk {
     }
 };
 
-// This block's range: sets the walk to its start and returns its number of
-// tiles.  `part`: kPagedWarps + 2 words of shared memory.
-__device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk &w, long long &first, long long &chunk,
-                                           long long *part)
+// This block's range: tiles whose cost begins in [at, stop).  Sets the walk to the
+// first of them; false if there is none.  `part`: kPagedWarps + 2 words of shared memory.
+__device__ __forceinline__ bool paged_range(const PagedDecodeParams &p, PagedWalk &w, long long &at, long long &stop,
+                                            long long *part)
 {
     long long *found = part + kPagedWarps;
+    const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
     if (p.aligned) {   // one unit per block
-        const int u = blockIdx.x % (p.c.Hkv * p.nsub);
-        w.b = blockIdx.x / (p.c.Hkv * p.nsub);
+        const int u = blockIdx.x % U;
+        w.b = blockIdx.x / U;
         w.h = u / p.nsub;
         w.sub = u - w.h * p.nsub;
         w.tile = 0;
         w.set(p, paged_count(p, w.b));
-        first = chunk = 0;
-        return w.nt;
+        at = 0;
+        stop = (long long)w.nt * kTileCost;
+        return true;
     }
-    const int B = p.c.B, U = p.c.Hkv * p.nsub, tid = threadIdx.x;
     const int slab = (B + kPagedThreads - 1) / kPagedThreads, b0 = min(B, tid * slab), b1 = min(B, b0 + slab);
     long long mine = 0, total;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) mine += paged_tiles(p, paged_count(p, b));
+    for (int b = b0; b < b1; ++b) mine += (long long)paged_tiles(p, paged_count(p, b)) * kTileCost + kUnitCost;
     long long before = block_scan<kPagedThreads>(mine, part, total);
     total *= U;
     const bool small = total < INT_MAX / 2;   // (a 32-bit division is a fraction of a 64-bit one)
-    chunk = small ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
-    first = blockIdx.x * chunk;
-    if (first >= total) return 0;
+    long long chunk = small ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
+    if (chunk < kTileCost) chunk = kTileCost;   // so that no range between two parts of a unit is without a tile
+    const long long first = blockIdx.x * chunk;
+    if (tid == 0) {
+        PagedRecord &r = p.rec[blockIdx.x];
+        r.head.b = r.tail.b = -1;
+        r.tiles = 0;
+        r.chunk = chunk;
+    }
+    if (first >= total) return false;
+    stop = first + chunk < total ? first + chunk : total;
     const long long x = small ? (unsigned)first / (unsigned)U : first / U;
     if (x >= before && x < before + mine) {
         int b = b0;
         for (;; ++b) {
-            const int nt = paged_tiles(p, paged_count(p, b));
-            if (x < before + nt) break;
-            before += nt;
+            const long long cost = (long long)paged_tiles(p, paged_count(p, b)) * kTileCost + kUnitCost;
+            if (x < before + cost) break;
+            before += cost;
         }
         found[0] = b;
         found[1] = before;
@@ -285,26 +300,31 @@ __device__ __forceinline__ int paged_range(const PagedDecodeParams &p, PagedWalk
     __syncthreads();
     w.b = (int)found[0];
     w.set(p, paged_count(p, w.b));
-    const long long off = first - U * found[1];   // below U * nt
-    const int u = small ? (int)((unsigned)off / (unsigned)w.nt) : (int)(off / w.nt);
+    const long long off = first - U * found[1], per = (long long)w.nt * kTileCost + kUnitCost;   // off < U * per
+    int u = small ? (int)((unsigned)off / (unsigned)per) : (int)(off / per);
+    const long long rem = off - u * per;
+    w.tile = (int)((rem + kTileCost - 1) / kTileCost);
+    at = first - rem + (long long)w.tile * kTileCost;
+    if (w.tile >= w.nt) {   // the range begins at a unit's end: the next one
+        at = first - rem + per;
+        w.tile = 0;
+        if (++u == U) {
+            u = 0;
+            if (++w.b == B) return false;
+            w.set(p, paged_count(p, w.b));
+        }
+    }
     w.h = u / p.nsub;
     w.sub = u - w.h * p.nsub;
-    w.tile = (int)(off - (long long)u * w.nt);
-    return (int)(total - first < chunk ? total - first : chunk);
-}
-
-// Records of a range for the join, written by thread 0 of the decode kernel.
-__device__ __forceinline__ void paged_record(const PagedDecodeParams &p, const PagedWalk &w, int tiles,
-                                             long long chunk)
-{
-    if (p.aligned) return;
-    PagedRecord &r = p.rec[blockIdx.x];
-    r.head.b = r.tail.b = -1;
-    r.tiles = tiles;
-    r.chunk = chunk;
-    r.b = w.b;
-    r.u = w.h * p.nsub + w.sub;
-    r.tile = w.tile;
+    if (at >= stop) return false;
+    if (tid == 0) {
+        PagedRecord &r = p.rec[blockIdx.x];
+        r.b = w.b;
+        r.u = u;
+        r.tile = w.tile;
+        r.at = at;
+    }
+    return true;
 }
 
 // 2^x; results below 2^-126 are 0.
@@ -364,8 +384,9 @@ __device__ __forceinline__ void paged_merge(const PagedDecodeParams &p, const Pa
     }
 }
 
-// The end of a unit's part [t0, w.tile] of a range: whether it is whole, and
-// what the join has to know if it is not.  Returns the slot of the part.
+// The end of a unit's part [t0, w.tile] of a range, at the tile that begins at
+// `at`: whether it is whole, and what the join has to know if it is not.  Returns
+// the slot of the part.
 __device__ __forceinline__ int paged_part(const PagedDecodeParams &p, const PagedWalk &w, int t0, long long at,
                                           bool &whole)
 {
@@ -374,8 +395,8 @@ __device__ __forceinline__ int paged_part(const PagedDecodeParams &p, const Page
     const int slot = t0 == 0 ? 1 : 0;
     if (threadIdx.x == 0) {
         PagedSpan &s = slot ? p.rec[blockIdx.x].tail : p.rec[blockIdx.x].head;
-        s.first = at - w.tile;
-        s.end = s.first + w.nt;
+        s.first = at - (long long)w.tile * kTileCost;
+        s.nt = w.nt;
         s.b = w.b;
         s.u = w.h * p.nsub + w.sub;
     }
@@ -445,16 +466,18 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
 // What the consumer has to know of a tile (below) lies beside the ring, so only
 // the loads walk through the sequences; the length of the sequence after the
 // walk's is on its way while the walk is in this one.
-struct __align__(16) PagedTile {
+struct PagedTile {
     uint32_t mask;     // slots attended to
     uint32_t copies;   // copies that fill them: 0, nothing to wait for
     int newrow;        // row of the new token if it is among them, else -1
     int n, b, h, sub, tile;
+    bool last;         // of the range (kept in the top bit of sub)
 };
 
 // Tiles kept beside the ring: with at most four places, the keys of tile i + 2
 // are asked for after tile i has been read, and tile i + 1 is still there.
 constexpr int kPagedAhead = 2;
+constexpr int kPagedTileBytes = 32;   // of a tile beside the ring
 
 template <typename T, typename E, int KB, int VB, int SLOTS, int ST, bool TMA>
 struct PagedFeed {
@@ -466,18 +489,21 @@ struct PagedFeed {
     const CUtensorMap *tm_k, *tm_v;
     uint8_t *ring;
     uint64_t *full;
-    PagedTile *tiles_at;
-    PagedWalk w;                 // the tile whose loads are next
-    int tiles, issued, place_in, place_out, warp, lane, entry, row;
+    int4 *tiles_at;
+    PagedWalk w;                 // the tile whose loads are next, and where its cost begins
+    long long at, stop;
+    bool done, values;           // no tile is left to begin; its values are next
+    int issued, place_in, place_out, warp, lane, entry, row;
     int next_len, next_pos;      // of sequence w.b + 1
     uint32_t copies, pending, phases;
     bool alive;                  // false once a wait ran out: tiles go by without loads and without slots
 
     __device__ __forceinline__ PagedFeed(const PagedDecodeParams &p_, const CUtensorMap *k, const CUtensorMap *v,
-                                         uint8_t *ring_, uint64_t *full_, PagedTile *at, const PagedWalk &w_, int tiles_)
-        : p(p_), tm_k(k), tm_v(v), ring(ring_), full(full_), tiles_at(at), w(w_), tiles(tiles_), issued(0), place_in(0),
-          place_out(0), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), row(-1), copies(0), pending(0), phases(0),
-          alive(true)
+                                         uint8_t *ring_, uint64_t *full_, uint8_t *tiles_, const PagedWalk &w_,
+                                         long long at_, long long stop_)
+        : p(p_), tm_k(k), tm_v(v), ring(ring_), full(full_), tiles_at(reinterpret_cast<int4 *>(tiles_)), w(w_), at(at_),
+          stop(stop_), done(false), values(false), issued(0), place_in(0), place_out(0), warp(threadIdx.x >> 5),
+          lane(threadIdx.x & 31), row(-1), copies(0), pending(0), phases(0), alive(true)
     {
         ahead();
         entry = paged_entry(p, w, slot());
@@ -505,8 +531,9 @@ struct PagedFeed {
     __device__ __forceinline__ void issue()
     {
         using namespace sm100;
-        if (issued >= 2 * tiles) return;
-        const bool isv = issued & 1;
+        if (done && !values) return;
+        const bool isv = values;
+        values = !values;
         const int group = p.box_rows < 4 ? 4 : p.box_rows < SLOTS ? p.box_rows : SLOTS;   // slots per copy
         if (!isv) {
             row = alive ? paged_entry_row(p, w, slot(), entry) : -1;
@@ -519,13 +546,16 @@ struct PagedFeed {
             copies = 0;
             if (TMA) copies = __ballot_sync(ALL, (lane & (group - 1)) == 0 && (held >> lane & (group == 32 ? ALL : (1u << group) - 1)));
             else if (fresh) row = -1;
+            at += kTileCost + (w.tile + 1 < w.nt ? 0 : kUnitCost);
+            done = at >= stop;
             if (lane == 0) {
-                int4 *to = reinterpret_cast<int4 *>(tiles_at + (issued >> 1) % kPagedAhead);
+                int4 *to = tiles_at + issued % kPagedAhead * 2;
                 to[0] = make_int4((int)mask, (int)copies, newrow, w.n);
-                to[1] = make_int4(w.b, w.h, w.sub, w.tile);
+                to[1] = make_int4(w.b, w.h, w.sub | (done ? INT_MIN : 0), w.tile);
             }
+            ++issued;
             if (!TMA) copies = held;
-            if ((issued >> 1) + 1 < tiles) advance();
+            if (!done) advance();
         }
         if (!alive) copies = 0;
         if (copies) {
@@ -571,7 +601,6 @@ struct PagedFeed {
                 __syncwarp();
             }
         }
-        ++issued;
         if (++place_in == ST) place_in = 0;
     }
     // the next place of the ring, once its copies have landed
@@ -628,7 +657,7 @@ struct PagedFeed {
     }
     __device__ __forceinline__ PagedTile tile(int it) const
     {
-        const int4 *from = reinterpret_cast<const int4 *>(tiles_at + it % kPagedAhead);
+        const int4 *from = tiles_at + it % kPagedAhead * 2;
         const int4 x = from[0], y = from[1];
         PagedTile t;
         t.mask = (uint32_t)x.x;
@@ -637,8 +666,9 @@ struct PagedFeed {
         t.n = x.w;
         t.b = y.x;
         t.h = y.y;
-        t.sub = y.z;
+        t.sub = y.z & INT_MAX;
         t.tile = y.w;
+        t.last = y.z < 0;
         return t;
     }
     // after a wait that ran out, let this warp's own copies land before leaving (bounded)
@@ -705,7 +735,7 @@ struct PagedMma {
     static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
     static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * kPagedMergeCols * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
-    static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * (int)sizeof(PagedTile);
+    static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
     static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
     static constexpr int BLOCKS = KB > 1 || VB > 1 ? 2 : 3;    // per SM
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -738,13 +768,11 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     launch_dependents();
 
     PagedWalk w;
-    long long at, chunk;
-    const int tiles = paged_range(p, w, at, chunk, reinterpret_cast<long long *>(obuf));
-    if (tid == 0) paged_record(p, w, tiles, chunk);
-    if (!tiles) return;
-    __syncthreads();   // the barriers are set, and the record is written before paged_part adds to it
+    long long at, stop;
+    if (!paged_range(p, w, at, stop, reinterpret_cast<long long *>(obuf))) return;
+    __syncthreads();   // the barriers are set, and obuf is free
     typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::ST * Cfg::Feed::PLACE, full,
-                            reinterpret_cast<PagedTile *>(smem + Cfg::OFF_TILE) + warp * kPagedAhead, w, tiles);
+                            smem + Cfg::OFF_TILE + warp * kPagedAhead * kPagedTileBytes, w, at, stop);
 #pragma unroll 1
     for (int s = 0; s < Cfg::ST - 1; ++s) feed.issue();
 
@@ -769,7 +797,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     };
     load_q(w);
     int t0 = 0;
-    for (int it = 0; it < tiles; ++it) {
+    for (int it = 0;; ++it) {
         __syncwarp();
         const PagedTile t = feed.tile(it);
         w = paged_unit(p, t);
@@ -869,7 +897,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                         sc[8 * n * p.stride + 8 * i + sv0] = sc[8 * n * p.stride + 8 * i + sv1] = -INFINITY;
         }
         // the next unit's queries are on their way while this one is finished
-        if (it + 1 < tiles && w.tile == w.nt - 1) {
+        if (!t.last && w.tile == w.nt - 1) {
             __syncwarp();
             load_q(paged_unit(p, feed.tile(it + 1)));
         }
@@ -904,9 +932,9 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 }
             }
         }
-        if (w.tile == w.nt - 1 || it == tiles - 1) {   // the unit, or its part in this range, ends
+        if (w.tile == w.nt - 1 || t.last) {   // the unit, or its part in this range, ends
             bool whole;
-            const int slot = paged_part(p, w, t0, at + it, whole);
+            const int slot = paged_part(p, w, t0, at, whole);
             if (w.n < 0) {
                 if (w.h == 0 && w.sub == 0 && tid == 0) report(kStatusCheck);
             } else {
@@ -941,6 +969,11 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
                 paged_store_position(p, w);
             }
         }
+        at += kTileCost + (w.tile + 1 < w.nt ? 0 : kUnitCost);
+        if (t.last) {
+            if (tid == 0 && !p.aligned) p.rec[blockIdx.x].tiles = it + 1;
+            break;
+        }
     }
     feed.drain();
 }
@@ -962,7 +995,7 @@ struct PagedSimt {
     static constexpr int OFF_P = OFF_Q + GM * D * 4;                       // [warp][16][GM] weights
     static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
-    static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * (int)sizeof(PagedTile);
+    static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
     static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
     static constexpr int BLOCKS = D > 64 || GM > 4 ? 2 : 3;                // per SM
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -1003,13 +1036,11 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
     launch_dependents();
 
     PagedWalk w;
-    long long at, chunk;
-    const int tiles = paged_range(p, w, at, chunk, reinterpret_cast<long long *>(obuf));
-    if (tid == 0) paged_record(p, w, tiles, chunk);
-    if (!tiles) return;
+    long long at, stop;
+    if (!paged_range(p, w, at, stop, reinterpret_cast<long long *>(obuf))) return;
     __syncthreads();
     typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::ST * Cfg::Feed::PLACE, full,
-                            reinterpret_cast<PagedTile *>(smem + Cfg::OFF_TILE) + warp * kPagedAhead, w, tiles);
+                            smem + Cfg::OFF_TILE + warp * kPagedAhead * kPagedTileBytes, w, at, stop);
 #pragma unroll 1
     for (int s = 0; s < Cfg::ST - 1; ++s) feed.issue();
 
@@ -1019,7 +1050,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
     float4 o[GM];
     float m[GM], l[GM];
     int t0 = 0;
-    for (int it = 0; it < tiles; ++it) {
+    for (int it = 0;; ++it) {
         __syncwarp();
         const PagedTile t = feed.tile(it);
         w = paged_unit(p, t);
@@ -1122,9 +1153,9 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
             feed.take(false);
             feed.issue();
         }
-        if (w.tile == w.nt - 1 || it == tiles - 1) {
+        if (w.tile == w.nt - 1 || t.last) {
             bool whole;
-            const int slot = paged_part(p, w, t0, at + it, whole);
+            const int slot = paged_part(p, w, t0, at, whole);
             if (w.n < 0) {
                 if (w.h == 0 && w.sub == 0 && tid == 0) report(kStatusCheck);
             } else {
@@ -1156,6 +1187,11 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                 paged_store_position(p, w);
             }
         }
+        at += kTileCost + (w.tile + 1 < w.nt ? 0 : kUnitCost);
+        if (t.last) {
+            if (tid == 0 && !p.aligned) p.rec[blockIdx.x].tiles = it + 1;
+            break;
+        }
     }
     feed.drain();
 }
@@ -1179,7 +1215,8 @@ __device__ __forceinline__ float2 paged_part_ml(const PagedDecodeParams &p, int 
 template <typename T>
 __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const PagedSpan &s, long long chunk, int range)
 {
-    const int g0 = paged_div(s.first, chunk), g1 = paged_div(s.end - 1, chunk), K = g1 - g0 + 1, dv = p.c.dv;
+    const int g0 = paged_div(s.first, chunk), g1 = paged_div(s.first + (s.nt - 1ll) * kTileCost, chunk);
+    const int K = g1 - g0 + 1, dv = p.c.dv;
     const int h = s.u / p.nsub, sub = s.u - h * p.nsub, rows = min(p.gs, p.g - sub * p.gs);
     const size_t hq0 = (size_t)s.b * p.Hq + h * p.g + sub * p.gs;
     const int E = rows * dv, per = (E + K - 1) / K, e0 = (range - g0) * per, e1 = min(E, e0 + per);
@@ -1268,13 +1305,17 @@ __global__ void __launch_bounds__(kPagedJoinThreads, 8) paged_join_kernel(const 
     // this block's tiles of the range
     const int from = (int)((long long)tiles * share / kPagedWeightBlocks);
     int left = (int)((long long)tiles * (share + 1) / kPagedWeightBlocks) - from;
-    for (int skip = from; skip > 0;) {
-        const int here = min(skip, w.nt - w.tile);
+    long long at = rec.at;
+    auto step = [&](int here) {   // past `here` tiles of the unit
+        at += (long long)here * kTileCost + (w.tile + here < w.nt ? 0 : kUnitCost);
         w.tile += here - 1;
         w.next(p, count);
+    };
+    for (int skip = from; skip > 0;) {
+        const int here = min(skip, w.nt - w.tile);
+        step(here);
         skip -= here;
     }
-    long long at = range * per_range + from;
     while (left > 0) {
         const int here = min(left, w.nt - w.tile);
         if (w.sub == 0 && w.n > 0) {
@@ -1282,8 +1323,10 @@ __global__ void __launch_bounds__(kPagedJoinThreads, 8) paged_join_kernel(const 
             __syncthreads();
             for (int j = tid; j < p.g; j += kPagedJoinThreads) {
                 const int sub = j / p.gs;
-                const long long first = at - w.tile + (long long)sub * w.nt;   // of this head's unit
-                const int g0 = paged_div(first, per_range), g1 = paged_div(first + w.nt - 1, per_range);
+                // where this head's unit begins: the units of a sequence follow one another
+                const long long cost = (long long)w.nt * kTileCost;
+                const long long first = at - (long long)w.tile * kTileCost + sub * (cost + kUnitCost);
+                const int g0 = paged_div(first, per_range), g1 = paged_div(first + cost - kTileCost, per_range);
                 if (g0 == g1) {
                     const float x = p.lse2[hq0 + j];
                     lse2[j] = x == -INFINITY ? INFINITY : x;   // nothing attended to: 2^(s - inf) = 0
@@ -1339,11 +1382,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads, 8) paged_join_kernel(const 
             }
         }
         left -= here;
-        at += here;
-        if (left > 0) {
-            w.tile += here - 1;
-            w.next(p, count);
-        }
+        if (left > 0) step(here);
     }
 }
 
