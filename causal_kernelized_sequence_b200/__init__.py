@@ -568,7 +568,7 @@ def la_paged_decode_step(q, k, v, k_pages, v_pages, block_table, lens, *, y=None
     ws, wsb, keep = _paged_workspace("la_paged_decode_workspace_bytes", workspace, dev,
                                      B, Hq, Hkv, dqk, dv, page, max_pages, int(weights is not None), dt)
     if y is None:
-        y = torch.empty((B, Hq, dv), dtype=T, device=dev)
+        y = torch.empty_like(q) if dv == dqk else q.new_empty((B, Hq, dv))
         y_ = y.data_ptr()
     _call(load_library().la_paged_decode_step, "la_paged_decode_step", dev,
           q_, k_, v_, y_, l_, kp, vp, tab, ln, w, w if wo is None else wo, ps, po, ws, wsb, B, Hq, Hkv, dqk, dv, P,

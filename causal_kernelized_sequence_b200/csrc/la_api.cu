@@ -724,7 +724,9 @@ static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_si
     pl->gs = (g + pl->nsub - 1) / pl->nsub;
     // as many blocks as an SM holds (BLOCKS of the kernels' configurations)
     const bool narrow = dqk <= 64 && dv <= 64;
-    pl->grid = kNumSms * (narrow && (pl->mma || pl->gs <= 4) ? 3 : 2);
+    pl->grid = kNumSms * (narrow && (pl->mma || pl->gs <= 4)                             ? 3
+                          : !narrow && !pl->tma && dtype == LA_F32 && pl->gs > 4 ? 1
+                                                                                 : 2);
     pl->tile = pl->mma ? 7 : 6;
     const int64_t tiles = (((int64_t)max_pages * page_size - 1) >> pl->tile) + 1, units = (int64_t)B * Hkv * pl->nsub;
     pl->stride = tiles << pl->tile;
@@ -793,7 +795,8 @@ static la_status paged_simt_run(PagedDecodeParams p, const PagedPlan &pl, cudaSt
 {
     using Cfg = PagedSimt<T, D, GM, TMA>;
     CUtensorMap tk = {}, tv = {};
-    p.box_rows = 0;
+    p.box_rows = 16;   // slots of a run that never leaves its page
+    while (p.c.page % p.box_rows) p.box_rows /= 2;
     if (TMA && paged_maps(&p, 16, LA_F32, &tk, &tv) != LA_OK) return LA_ERR_CUDA;
     if (set_smem<paged_decode_simt_kernel<T, D, GM, TMA>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
     return launch_pdl(paged_decode_simt_kernel<T, D, GM, TMA>, pl.grid, kPagedThreads, Cfg::SMEM, st, tk, tv, p);
@@ -1440,11 +1443,15 @@ la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_tabl
     p.newlen = lens_out == lens ? p.movers + (size_t)B * Hkv * p.maxmoves : nullptr;
     p.elem = (int)elem_size(dtype);
     p.width = rows16(dqk, dtype) && rows16(dv, dtype) ? 16 : p.elem;
-    // blocks per (b, h): as many as run at once (four on an SM), with
-    // at least 1024 slots each
+    // blocks per (b, h): as many as run at once (four on an SM), with at least 1024
+    // slots each, and so many that the keys of twice the budget fit their shared
+    // memory (a longer sequence is right too: its keys are made anew in each sweep)
     const int64_t units = (int64_t)B * Hkv, cap = (int64_t)max_pages * page_size;
+    const int64_t likely = cap < 2 * (int64_t)budget + 1024 ? cap : 2 * (int64_t)budget + 1024;
     int cs = 1;
-    while (cs < kEvictMaxCluster && units * cs * 2 <= 4 * kNumSms && cap >= (int64_t)cs * 2 * 1024) cs *= 2;
+    while (cs < kEvictMaxCluster &&
+           ((units * cs * 2 <= 4 * kNumSms && cap >= (int64_t)cs * 2 * 1024) || likely > (int64_t)cs * kEvictMaxKeys))
+        cs *= 2;
     if (units * cs >= (int64_t)1 << 31) return LA_ERR_INVALID_ARG;
     const int64_t slice = (cap + cs * kEvictThreads - 1) / (cs * kEvictThreads) * kEvictThreads;
     p.keys = (int)(slice < kEvictMaxKeys ? slice : kEvictMaxKeys);

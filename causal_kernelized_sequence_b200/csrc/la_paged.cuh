@@ -422,6 +422,17 @@ __device__ __forceinline__ int paged_entry_row(const PagedDecodeParams &p, const
     return (entry * c.Hkv + w.h) * c.page + off;
 }
 
+// The first `bytes` of 16 bytes from global to shared memory, zeros after them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
@@ -460,7 +471,9 @@ __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t r)
 // place: slots of a page are neighbouring rows of the pool, so a box of
 // `box_rows` rows (32, 16, 8 or 4, whichever divides the page size) is one copy
 // per block; pages of other sizes gather four rows by index.  Rows that do not
-// start on 16 bytes cannot be copied by TMA: the lanes load their elements.
+// start on 16 bytes cannot be copied by TMA: the 16-byte pieces that cover a run
+// of rows come by cp.async into a ring of their own, and the lanes spread the
+// elements into one place, as floats, when they are needed.
 // Nothing but the wait for its own copies orders a warp inside a unit.
 //
 // What the consumer has to know of a tile (below) lies beside the ring, so only
@@ -485,6 +498,10 @@ struct PagedFeed {
     static constexpr uint32_t ALL = 0xffffffffu;
     static constexpr int BLOCK = SLOTS * 128, PLACE = (KB > VB ? KB : VB) * BLOCK;
     static constexpr int COLS = 128 / sizeof(E);   // elements of a block's row: E in shared memory, T in the pool
+    // a warp's shared memory: the ring; or one place, the ring of raw rows (at worst
+    // every row a run of its own) and where each slot's row begins in it
+    static constexpr int RAW = SLOTS * ((KB > VB ? KB : VB) * COLS * (int)sizeof(T) + 30) / 16 * 16;
+    static constexpr int BYTES = TMA ? ST * PLACE : (PLACE + ST * (RAW + SLOTS * 2) + 127) / 128 * 128;
     const PagedDecodeParams &p;
     const CUtensorMap *tm_k, *tm_v;
     uint8_t *ring;
@@ -531,7 +548,10 @@ struct PagedFeed {
     __device__ __forceinline__ void issue()
     {
         using namespace sm100;
-        if (done && !values) return;
+        if (done && !values) {
+            if (!TMA) cp_async_commit();   // every load is a group, so that the wait can count them
+            return;
+        }
         const bool isv = values;
         values = !values;
         const int group = p.box_rows < 4 ? 4 : p.box_rows < SLOTS ? p.box_rows : SLOTS;   // slots per copy
@@ -546,6 +566,7 @@ struct PagedFeed {
             copies = 0;
             if (TMA) copies = __ballot_sync(ALL, (lane & (group - 1)) == 0 && (held >> lane & (group == 32 ? ALL : (1u << group) - 1)));
             else if (fresh) row = -1;
+            if (!TMA) copies = held;
             at += kTileCost + (w.tile + 1 < w.nt ? 0 : kUnitCost);
             done = at >= stop;
             if (lane == 0) {
@@ -554,7 +575,6 @@ struct PagedFeed {
                 to[1] = make_int4(w.b, w.h, w.sub | (done ? INT_MIN : 0), w.tile);
             }
             ++issued;
-            if (!TMA) copies = held;
             if (!done) advance();
         }
         if (!alive) copies = 0;
@@ -582,38 +602,54 @@ struct PagedFeed {
                 }
                 pending |= 1u << place_in;
             } else {
-                // eight lanes per slot, four elements at a time
-                const int d = isv ? p.c.dv : p.c.dqk;
-                const T *pool = (const T *)(isv ? p.c.vp : p.c.kp);
-#pragma unroll 1
-                for (int s0 = 0; s0 < SLOTS; s0 += 4) {
-                    const int s = s0 + (lane >> 3), r = __shfl_sync(ALL, row, s);
-#pragma unroll 1
-                    for (int j = 0; j * 32 < d; ++j) {
-                        const int col = j * 32 + (lane & 7) * 4;
-                        float x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = r >= 0 && col + e < d ? ld(pool + (size_t)r * d + col + e) : 0.f;
-                        *reinterpret_cast<float4 *>(dst + j * BLOCK + s * 128 + (((lane ^ s) & 7) << 4)) =
-                            make_float4(x[0], x[1], x[2], x[3]);
-                    }
+                const int rb = (isv ? p.c.dv : p.c.dqk) * (int)sizeof(T), run = p.box_rows < SLOTS ? p.box_rows : SLOTS;
+                const int stride = (run * rb + 30) / 16 * 16;   // a run and what its alignment adds
+                const uint8_t *pool = (const uint8_t *)(isv ? p.c.vp : p.c.kp);
+                const size_t end = (size_t)p.c.num_pages * p.c.Hkv * p.c.page * rb;
+                const uint32_t raw = sm100::smem_addr(ring + PLACE + place_in * RAW);
+                for (int s = 0; s < SLOTS; s += run) {
+                    // a run lies in one page: its first slot is held if any is
+                    const int first = __shfl_sync(ALL, row, s);
+                    if (first < 0) continue;
+                    const size_t start = (size_t)first * rb, from = start & ~(size_t)15;
+                    const int skip = (int)(start - from), at = s / run * stride;
+                    for (int i = lane * 16; i < skip + run * rb; i += 512)
+                        cp_async16(raw + at + i, pool + from + i, from + i + 16 <= end ? 16 : (int)(end - from - i));
+                    if (lane < run) offsets()[place_in * SLOTS + s + lane] = (uint16_t)(at + skip + lane * rb);
                 }
-                __syncwarp();
             }
         }
+        if (!TMA) cp_async_commit();
         if (++place_in == ST) place_in = 0;
     }
-    // the next place of the ring, once its copies have landed
-    __device__ __forceinline__ uint8_t *take(bool copied)
+    __device__ __forceinline__ uint16_t *offsets() const { return reinterpret_cast<uint16_t *>(ring + PLACE + ST * RAW); }
+    // the next place of the ring, once its copies (a mask of them) have landed; rows of d elements
+    __device__ __forceinline__ uint8_t *take(uint32_t copied, int d)
     {
-        if (TMA && copied && alive) {
-            alive = __all_sync(ALL, sm100::mbar_wait(full + place_out, phases >> place_out & 1));
-            if (alive) {
-                phases ^= 1u << place_out;
-                pending &= ~(1u << place_out);
+        uint8_t *at = ring;
+        if constexpr (TMA) {
+            if (copied && alive) {
+                alive = __all_sync(ALL, sm100::mbar_wait(full + place_out, phases >> place_out & 1));
+                if (alive) {
+                    phases ^= 1u << place_out;
+                    pending &= ~(1u << place_out);
+                }
             }
+            at += place_out * PLACE;
+        } else {
+            cp_async_wait<ST - 2>();
+            __syncwarp();
+            const T *raw = reinterpret_cast<const T *>(ring + PLACE + place_out * RAW);
+#pragma unroll 4
+            for (int s = 0; s < SLOTS; ++s) {
+                const T *from = raw + offsets()[place_out * SLOTS + s] / sizeof(T);
+                float *to = reinterpret_cast<float *>(ring + s * 128 + ((lane >> 2 ^ (s & 7)) << 4)) + (lane & 3);
+                if (copied >> s & 1)
+                    for (int j = 0; j * 32 + lane < (d + 31) / 32 * 32; ++j)
+                        to[j * (BLOCK / 4)] = j * 32 + lane < d ? ld(from + j * 32 + lane) : 0.f;
+            }
+            __syncwarp();
         }
-        uint8_t *at = ring + place_out * PLACE;
         if (++place_out == ST) place_out = 0;
         return at;
     }
@@ -732,17 +768,18 @@ struct PagedMma {
     static constexpr int ST = KB > 1 || VB > 1 ? 3 : 4;
     using Feed = PagedFeed<__nv_bfloat16, __nv_bfloat16, KB, VB, 32, ST, true>;
     static constexpr int BLOCK = Feed::BLOCK;
-    static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
+    static constexpr int OFF_O = kPagedWarps * Feed::BYTES;
     static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * kPagedMergeCols * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
     static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
     static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
     static constexpr int BLOCKS = KB > 1 || VB > 1 ? 2 : 3;    // per SM
+    static constexpr int REGS = BLOCKS == 3 ? 168 : HI ? 248 : 224;   // 224: the join fits beside two blocks
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 template <int DQ, int DV, bool HI>
-__global__ void __launch_bounds__(kPagedThreads, PagedMma<DQ, DV, HI>::BLOCKS)
+__global__ void __launch_bounds__(kPagedThreads) __maxnreg__((PagedMma<DQ, DV, HI>::REGS))
 paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const PagedDecodeParams p)
 {
@@ -771,7 +808,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
     long long at, stop;
     if (!paged_range(p, w, at, stop, reinterpret_cast<long long *>(obuf))) return;
     __syncthreads();   // the barriers are set, and obuf is free
-    typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::ST * Cfg::Feed::PLACE, full,
+    typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::Feed::BYTES, full,
                             smem + Cfg::OFF_TILE + warp * kPagedAhead * kPagedTileBytes, w, at, stop);
 #pragma unroll 1
     for (int s = 0; s < Cfg::ST - 1; ++s) feed.issue();
@@ -814,7 +851,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
         const uint32_t mask = t.mask;
         const int rows = w.rows(p);
         float *const sc = p.scores ? p.scores + (w.hq(p) + r) * p.stride + (w.tile << 7) + warp * 32 : nullptr;
-        uint8_t *kp = feed.take(t.copies);
+        uint8_t *kp = feed.take(t.copies, c.dqk);
         feed.issue();   // into the place before, which every lane has used; with it the next tile is known
         uint32_t hi[4][NR], lo[4][NR];   // P: [slots 8 i + sv.][row]
         if (mask && feed.alive) {
@@ -901,7 +938,7 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
             __syncwarp();
             load_q(paged_unit(p, feed.tile(it + 1)));
         }
-        uint8_t *vp = feed.take(t.copies);
+        uint8_t *vp = feed.take(t.copies, c.dv);
         feed.issue();
         if (mask && feed.alive) {
             if (t.newrow >= 0) feed.patch(vp, (const T *)p.v + w.bh(p) * c.dv, (T *)c.vp, c.dv, Cfg::VB, t);
@@ -985,19 +1022,19 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 template <typename T, int D, int GM, bool TMA>
 struct PagedSimt {
     static constexpr int NB = D / 32;                // 32-column blocks
-    static constexpr int ST = D > 64 && GM > 4 ? 2 : 3;
+    static constexpr int ST = !TMA || (D > 64 && GM > 4) ? 2 : 3;
     static constexpr int OR = GM < 8 ? GM : 8;       // rows merged at once
     using Feed = PagedFeed<T, float, NB, NB, 16, ST, TMA>;
     static constexpr int BLOCK = Feed::BLOCK;
     static constexpr int LR = D / 4, TP = 32 / LR;   // lanes per value row, rows per pass
-    static constexpr int OFF_O = kPagedWarps * ST * Feed::PLACE;
+    static constexpr int OFF_O = kPagedWarps * Feed::BYTES;
     static constexpr int OFF_Q = OFF_O + kPagedWarps * OR * kPagedMergeCols * 4;   // [GM][D] queries, shared by the warps
     static constexpr int OFF_P = OFF_Q + GM * D * 4;                       // [warp][16][GM] weights
     static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
     static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
     static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
-    static constexpr int BLOCKS = D > 64 || GM > 4 ? 2 : 3;                // per SM
+    static constexpr int BLOCKS = D > 64 && GM > 4 && !TMA && sizeof(T) == 4 ? 1 : D > 64 || GM > 4 ? 2 : 3;   // per SM
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -1039,7 +1076,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
     long long at, stop;
     if (!paged_range(p, w, at, stop, reinterpret_cast<long long *>(obuf))) return;
     __syncthreads();
-    typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::ST * Cfg::Feed::PLACE, full,
+    typename Cfg::Feed feed(p, &tm_k, &tm_v, smem + warp * Cfg::Feed::BYTES, full,
                             smem + Cfg::OFF_TILE + warp * kPagedAhead * kPagedTileBytes, w, at, stop);
 #pragma unroll 1
     for (int s = 0; s < Cfg::ST - 1; ++s) feed.issue();
@@ -1072,7 +1109,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
             }
         }
         const uint32_t mask = t.mask;
-        uint8_t *kp = feed.take(t.copies);
+        uint8_t *kp = feed.take(t.copies, c.dqk);
         feed.issue();
         if (mask && feed.alive) {
             if (t.newrow >= 0) feed.patch(kp, (const T *)p.k + w.bh(p) * c.dqk, (T *)c.kp, c.dqk, Cfg::NB, t);
@@ -1122,7 +1159,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                 o[n].w *= al;
             }
             __syncwarp();
-            uint8_t *vp = feed.take(t.copies);
+            uint8_t *vp = feed.take(t.copies, c.dv);
             feed.issue();
             if (t.newrow >= 0 && feed.alive) feed.patch(vp, (const T *)p.v + w.bh(p) * c.dv, (T *)c.vp, c.dv, Cfg::NB, t);
             const uint32_t vs = smem_addr(vp) + off_v;
@@ -1133,14 +1170,20 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                     const int row = i * Cfg::TP + vrow;
                     const float4 x = lds_f4(vs + row * 128 + (((lane ^ row) & 7) << 4));
                     const float *pp = ps + row * GM;
+                    constexpr int F = GM < 4 ? GM : 4;   // weights per load
 #pragma unroll
-                    for (int n = 0; n < GM; ++n) {
-                        if (n >= rows) break;
-                        const float f = pp[n];
-                        o[n].x = fmaf(f, x.x, o[n].x);
-                        o[n].y = fmaf(f, x.y, o[n].y);
-                        o[n].z = fmaf(f, x.z, o[n].z);
-                        o[n].w = fmaf(f, x.w, o[n].w);
+                    for (int n0 = 0; n0 < GM; n0 += F) {
+                        if (n0 >= rows) break;
+                        __align__(16) float f[F];
+                        if constexpr (F == 4) *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(pp + n0);
+                        else f[0] = pp[0];
+#pragma unroll
+                        for (int n = n0; n < n0 + F; ++n) {
+                            o[n].x = fmaf(f[n - n0], x.x, o[n].x);
+                            o[n].y = fmaf(f[n - n0], x.y, o[n].y);
+                            o[n].z = fmaf(f[n - n0], x.z, o[n].z);
+                            o[n].w = fmaf(f[n - n0], x.w, o[n].w);
+                        }
                     }
                 }
             }
@@ -1150,7 +1193,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                 for (int n = 0; n < rows; ++n)
                     for (int i = 0; i < 2; ++i)
                         p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + r] = -INFINITY;
-            feed.take(false);
+            feed.take(0, c.dv);
             feed.issue();
         }
         if (w.tile == w.nt - 1 || t.last) {
@@ -1274,7 +1317,7 @@ __device__ __forceinline__ void paged_join(const PagedDecodeParams &p, const Pag
 // One block per range joins; with weights kPagedWeightBlocks more add the
 // weights of a part of the range's tiles each.
 template <typename T, bool WEIGHTS>
-__global__ void __launch_bounds__(kPagedJoinThreads, 8) paged_join_kernel(const PagedDecodeParams p)
+__global__ void __launch_bounds__(kPagedJoinThreads, 9) paged_join_kernel(const PagedDecodeParams p)
 {
     sm100::grid_dependency_wait();
     sm100::launch_dependents();
