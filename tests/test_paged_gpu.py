@@ -84,6 +84,7 @@ SHAPES = [  # dtype, Hq, Hkv, dqk, dv, page
     (BF16, 7, 1, 8, 8, 100), (BF16, 1, 1, 127, 5, 16),
     (F32, 4, 4, 64, 64, 16), (F32, 8, 2, 128, 128, 64), (F32, 20, 1, 64, 32, 8), (F32, 6, 3, 24, 40, 10),
     (F32, 5, 1, 33, 20, 7), (F32, 1, 1, 1, 128, 1), (F32, 17, 1, 128, 128, 128),
+    (BF16, 128, 1, 64, 64, 16), (F32, 65, 1, 32, 40, 4), (BF16, 6, 2, 65, 127, 48), (F32, 9, 3, 127, 66, 2),
 ]
 
 
@@ -107,7 +108,7 @@ def test_decode_step(dtype, Hq, Hkv, dqk, dv, page, new):
         lse = torch.full((B, Hq), 3.0, device=DEV)
         wo = torch.full_like(wd, -7.0)
         more = {"weights": wd, "weights_out": wo} if weights else {}
-        if new and weights:
+        if new:
             more.update(positions=pd, pos=posd)
         y = la.la_paged_decode_step(qd, kd, vd, kpd, vpd, td, ld, lse=lse, **more)
         sync()
@@ -124,7 +125,7 @@ def test_decode_step(dtype, Hq, Hkv, dqk, dv, page, new):
             k[:, :, None], v[:, :, None], kp, vp, table, lens, positions=posn, pos=pos)
         as_int = torch.int16 if dtype == BF16 else torch.int32
         assert torch.equal(kpd.cpu().view(as_int), kr.view(as_int)) and torch.equal(vpd.cpu().view(as_int), vr.view(as_int))
-        assert torch.equal(pd.cpu(), pr if new and weights else posn)
+        assert torch.equal(pd.cpu(), pr)
         if weights:   # in place gives the same bits
             wd2 = w.to(DEV)
             y2 = la.la_paged_decode_step(qd, kd, vd, kpd, vpd, td, ld, weights=wd2)
@@ -308,6 +309,48 @@ def test_evict(dtype, Hkv, dqk, dv, page, lens, budget, recent, ties):
         assert torch.equal(kpd.cpu().view(as_int), kr.view(as_int)) and torch.equal(ld.cpu(), lr)
 
 
+@pytest.mark.parametrize("B,Hkv,n,budget,recent,ties", [
+    (1, 1, 110000, 30000, 1000, False),     # a cluster whose slices are too long for the keys to be kept
+    (300, 1, 13000, 500, 64, True),         # the same for single blocks; more warps' rounds than one
+    (40, 4, 3000, 2900, 0, True), (5, 3, 9000, 4000, 4000, False)])
+def test_evict_long(B, Hkv, n, budget, recent, ties):
+    """Against a stable sort of every head's slots."""
+    page, d = 64, 8
+    mp = -(-n // page)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    kp, vp = (torch.randn(B * mp, Hkv, page, d, generator=g, device=DEV).to(BF16) for _ in range(2))
+    table = torch.randperm(B * mp, generator=g, device=DEV).view(B, mp).int()
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    lens[1:][-1:] = budget + 1
+    w = torch.rand(B, Hkv, mp * page, generator=g, device=DEV)
+    if ties:
+        w = (w * 9).floor()
+    posn = torch.rand(B, Hkv, mp * page, generator=g, device=DEV).argsort(-1).int()
+    pos = torch.full((B,), mp * page, dtype=torch.int32, device=DEV)
+    t = torch.arange(n, device=DEV).expand(B, Hkv, n)
+    live = t < lens[:, None, None]
+    key = torch.where(posn[..., :n] >= mp * page - recent, math.inf, w[..., :n]) if recent else w[..., :n]
+    order = torch.where(live, key, -math.inf).sort(dim=-1, descending=True, stable=True).indices
+    keep = torch.zeros_like(live).scatter_(2, order[..., :budget], True) & live
+    # the slot that each one below the budget takes: itself, or the next mover
+    src = t[..., :budget].clone()
+    hole, mover = (~keep & live)[..., :budget], keep & (t >= budget)
+    src[hole] = t[mover]                    # both in (b, h, ascending slot) order, equally many per head
+    assert torch.equal(hole.sum(-1), mover.sum(-1))
+    flat = lambda slots: ((table.long()[:, None].expand(B, Hkv, mp).gather(2, slots // page) * Hkv
+                           + torch.arange(Hkv, device=DEV)[None, :, None]) * page + slots % page)
+    to, frm = flat(t[..., :budget].contiguous()), flat(src)
+    kr, vr = kp.clone(), vp.clone()
+    kr.view(-1, d)[to], vr.view(-1, d)[to] = kp.view(-1, d)[frm], vp.view(-1, d)[frm]
+    w0, p0 = w.clone(), posn.clone()
+    la.la_paged_evict(kp, vp, table, lens, w, budget, recent=recent, positions=posn, pos=pos)
+    sync()
+    assert (lens == budget).all()
+    assert torch.equal(w[..., :budget], w0.gather(2, src)) and torch.equal(posn[..., :budget], p0.gather(2, src))
+    assert torch.equal(w[..., budget:], w0[..., budget:])
+    assert torch.equal(kp, kr) and torch.equal(vp, vr)
+
+
 def test_evict_recent_alone_exceed_the_budget():
     """Every token recent (positions not distinct): the weights decide among them."""
     kp, vp, table, lens = cache(2, BF16, 1, 1, 8, 8, 16, 4, [64], used=[4])
@@ -412,6 +455,50 @@ def test_captured_step_follows_the_lengths():
     assert torch.equal(runs[0][1], runs[1][1]) and torch.equal(runs[0][2], runs[1][2])
 
 
+def test_captured_append_step_and_evict():
+    """One graph of an append, a step and an eviction in place, replayed: the eager calls' bits."""
+    B, Hq, Hkv, d, page, mp, budget = 2, 4, 2, 64, 16, 30, 300
+    g = torch.Generator().manual_seed(14)
+    kp, vp, table, lens = cache(43, BF16, B, Hkv, d, d, page, mp, [290, 20], used=[mp] * B)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF16).to(DEV)
+    kf, vf = rnd(B, Hkv, 40, d), rnd(B, Hkv, 40, d)
+    q, k, v = rnd(B, Hq, d), rnd(B, Hkv, d), rnd(B, Hkv, d)
+    res = []
+    for captured in (False, True):
+        kpd, vpd, td, ld = to_dev(kp, vp, table, lens)
+        w = torch.rand(B, Hkv, mp * page, generator=torch.Generator().manual_seed(1)).to(DEV)
+        ps = torch.arange(mp * page, dtype=torch.int32, device=DEV).expand(B, Hkv, -1).contiguous()
+        pos, y = ld.clone(), torch.empty(B, Hq, d, dtype=BF16, device=DEV)
+
+        def steps():
+            la.la_paged_cache_fill(kf, vf, kpd, vpd, td, ld, weights=w, positions=ps, pos=pos)
+            ld.add_(40)
+            pos.add_(40)
+            la.la_paged_decode_step(q, k, v, kpd, vpd, td, ld, y=y, weights=w, positions=ps, pos=pos)
+            ld.add_(1)
+            pos.add_(1)
+            la.la_paged_evict(kpd, vpd, td, ld, w, budget, recent=32, positions=ps, pos=pos)
+        if captured:
+            keep = [x.clone() for x in (kpd, vpd, ld, w, ps, pos)]
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                steps()
+            torch.cuda.current_stream().wait_stream(side)
+            sync()
+            for x, c in zip((kpd, vpd, ld, w, ps, pos), keep):
+                x.copy_(c)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                steps()
+        for _ in range(8):
+            graph.replay() if captured else steps()
+        sync()
+        res.append([x.cpu() for x in (kpd.view(torch.int16), vpd.view(torch.int16), ld, w, ps, pos, y)])
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert res[0][2].tolist() == [300, 300]
+
+
 def test_steps_on_two_streams_with_their_own_workspaces():
     """Two steps in flight at once on different caches give what they give alone."""
     d, page, mp, Hq, Hkv = 64, 16, 260, 4, 2
@@ -474,6 +561,25 @@ def test_bad_length_leaves_the_sequence_alone(bad):
         _reported()
         own = table[1].long()
         assert torch.equal(kp2[own], kp[own]) and torch.equal(vp2[own], vp[own]) and torch.equal(w2[1], w[1])
+
+
+def test_narrow_and_wide_tables_agree():
+    """The same short sequences behind a table of few pages (one block per unit) and of many (ranges and a join)."""
+    for dtype, Hq, Hkv, d in ((BF16, 8, 2, 64), (BF16, 24, 2, 128), (F32, 4, 4, 64), (BF16, 3, 1, 33)):
+        lens = [0, 1, 31, 128, 129, 200]
+        kp, vp, table, ln = to_dev(*cache(71, dtype, len(lens), Hkv, d, d, 16, 13, lens))
+        wide = torch.full((len(lens), 4000), -1, dtype=torch.int32, device=DEV)
+        wide[:, :13] = table
+        q = torch.randn(len(lens), Hq, d, device=DEV).to(dtype)
+        n1 = la.la_paged_kernel_plan(1, len(lens), Hq, Hkv, d, d, 16, 13, False, la._dtype_code(q))[0]
+        n2 = la.la_paged_kernel_plan(1, len(lens), Hq, Hkv, d, d, 16, 4000, False, la._dtype_code(q))[0]
+        assert (n1, n2) == (1, 2)
+        ref = orc.decode(*(t.cpu() for t in (q,)), None, None, *(t.cpu() for t in (kp, vp, table, ln)))
+        for tab in (table, wide):
+            lse = torch.empty(len(lens), Hq, device=DEV)
+            y = la.la_paged_decode_step(q, None, None, kp, vp, tab, ln, lse=lse)
+            sync()
+            check_step(dtype, 200, d, (y, lse, None), (*ref[:2], None, *ref[3:]))
 
 
 @pytest.mark.parametrize("bad", [-1, 20, 1 << 30, -(1 << 31)])

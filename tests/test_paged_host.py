@@ -168,3 +168,21 @@ def test_oracle_evict_example():
     # kept: slot 4 (recent), then 0 and 2 (0.5, ties to the lowest slots); slot 1 is dropped, 4 takes its place
     assert l2.tolist() == [3] and p2[0, 0, :3].tolist() == [0, 4, 2] and w2[0, 0, :3].tolist() == pytest.approx([0.5, 0.2, 0.5])
     assert k2[1, 0, :, 0].tolist() == [3.0, 1.0, 5.0] and k2[0, 0].equal(kp[0, 0])
+
+
+def test_every_dependent_paged_launch_waits_and_releases():
+    """The paged kernels are launched as programmatic dependents: each waits for the kernel before it and releases the
+    one after it."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(la.__file__), "csrc")
+    src = open(os.path.join(csrc, "la_paged.cuh")).read()
+    api = open(os.path.join(csrc, "la_api.cu")).read()
+    names = re.findall(r"\b(paged_\w+_kernel)\s*\(const", src)
+    assert len(names) == 6, names
+    for name in names:
+        body = src[src.index(name + "(const"):]
+        body = body[:body.index("\n}\n")]
+        assert "grid_dependency_wait()" in body and "launch_dependents()" in body, name
+        assert re.search(r"launch_pdl(_cluster)?\(" + name, api), name
+        assert not re.search(name + r"[^;(]*<<<", api), name
