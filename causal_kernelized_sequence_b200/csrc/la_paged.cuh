@@ -591,13 +591,14 @@ struct PagedFeed {
                 }
                 __syncwarp();
                 if (copies >> lane & 1) {
+                    const uint64_t policy = policy_evict_first();
 #pragma unroll
                     for (int j = 0; j < (KB > VB ? KB : VB); ++j) {
                         if (j >= (isv ? VB : KB)) break;
                         if (p.box_rows < 4)
                             tma_gather4(dst + j * BLOCK + lane * 128, map, full + place_in, j * COLS, max(row, 0), y1, y2, y3);
                         else
-                            tma_load_2d(dst + j * BLOCK + lane * 128, map, full + place_in, j * COLS, row);
+                            tma_load_2d_hint(dst + j * BLOCK + lane * 128, map, full + place_in, j * COLS, row, policy);
                     }
                 }
                 pending |= 1u << place_in;
