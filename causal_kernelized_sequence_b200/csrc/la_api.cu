@@ -157,6 +157,24 @@ la_status set_smem(size_t bytes)
     return LA_OK;
 }
 
+// Ask for the SM's whole shared memory beside a kernel that uses little of it
+// (once per kernel and device, as above).  A launch that begins while the
+// kernel's last blocks leave would otherwise find SMs divided for the little,
+// and could place fewer of its blocks there until they are empty.
+template <auto kernel>
+la_status set_carveout()
+{
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LA_ERR_CUDA;
+    if (done[dev].load(std::memory_order_acquire)) return LA_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+        cudaSuccess)
+        return LA_ERR_CUDA;
+    done[dev].store(true, std::memory_order_release);
+    return LA_OK;
+}
+
 // Kernel selection, shared by the entry points and la_kernel_plan.
 enum class Path { Invalid, FwdSimt, FwdSplit, FwdTc, BwdSimt, BwdTc, DecodeSimt, DecodeVec };
 
@@ -778,7 +796,7 @@ static la_status paged_mma_run(PagedDecodeParams p, const PagedPlan &pl, cudaStr
     using Cfg = PagedMma<DQ, DV, HI>;
     CUtensorMap tk, tv;
     if (paged_maps(&p, 32, LA_BF16, &tk, &tv) != LA_OK) return LA_ERR_CUDA;
-    if (set_smem<paged_decode_mma_kernel<DQ, DV, HI>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
+    if (set_smem<paged_decode_mma_kernel<DQ, DV, HI>>(Cfg::SMEM) != LA_OK || set_carveout<paged_decode_mma_kernel<DQ, DV, HI>>() != LA_OK) return LA_ERR_CUDA;
     return launch_pdl(paged_decode_mma_kernel<DQ, DV, HI>, pl.grid, kPagedThreads, Cfg::SMEM, st, tk, tv, p);
 }
 
@@ -801,7 +819,7 @@ static la_status paged_simt_run(PagedDecodeParams p, const PagedPlan &pl, cudaSt
     p.box_rows = 16;   // slots of a run that never leaves its page
     while (p.c.page % p.box_rows) p.box_rows /= 2;
     if (TMA && paged_maps(&p, 16, LA_F32, &tk, &tv) != LA_OK) return LA_ERR_CUDA;
-    if (set_smem<paged_decode_simt_kernel<T, D, GM, TMA>>(Cfg::SMEM) != LA_OK) return LA_ERR_CUDA;
+    if (set_smem<paged_decode_simt_kernel<T, D, GM, TMA>>(Cfg::SMEM) != LA_OK || set_carveout<paged_decode_simt_kernel<T, D, GM, TMA>>() != LA_OK) return LA_ERR_CUDA;
     return launch_pdl(paged_decode_simt_kernel<T, D, GM, TMA>, pl.grid, kPagedThreads, Cfg::SMEM, st, tk, tv, p);
 }
 
@@ -814,6 +832,16 @@ static la_status paged_simt(const PagedDecodeParams &p, const PagedPlan &pl, cud
     }
     if (pl.gs == 1) return paged_simt_run<T, 128, 1, TMA>(p, pl, st);
     return pl.gs <= 4 ? paged_simt_run<T, 128, 4, TMA>(p, pl, st) : paged_simt_run<T, 128, 16, TMA>(p, pl, st);
+}
+
+template <typename T, bool WEIGHTS>
+static la_status paged_join(const PagedDecodeParams &p, const PagedPlan &pl, cudaStream_t st)
+{
+    const int grid = pl.grid * (WEIGHTS ? kPagedWeightBlocks + 1 : 1);
+    // (93 us a step without it, 57 with it, for 16 fp32 sequences of up to 4096 slots,
+    // step after step: some SMs took two of the next step's blocks instead of three)
+    if (set_carveout<paged_join_kernel<T, WEIGHTS>>() != LA_OK) return LA_ERR_CUDA;
+    return launch_pdl(paged_join_kernel<T, WEIGHTS>, grid, kPagedJoinThreads, 0, st, p);
 }
 
 // The eviction with U row pairs in flight per warp, BLOCKS blocks on an SM.
@@ -1384,12 +1412,8 @@ la_status la_paged_decode_step(const void *q, const void *k, const void *v, void
                          : dtype == LA_F32  ? paged_simt<float, false>(p, pl, st)
                                             : paged_simt<__nv_bfloat16, false>(p, pl, st);
     if (s1 != LA_OK || pl.aligned) return s1;
-    const int jg = weights_in ? pl.grid * (kPagedWeightBlocks + 1) : pl.grid;
-    if (dtype == LA_F32)
-        return weights_in ? launch_pdl(paged_join_kernel<float, true>, jg, kPagedJoinThreads, 0, st, p)
-                          : launch_pdl(paged_join_kernel<float, false>, jg, kPagedJoinThreads, 0, st, p);
-    return weights_in ? launch_pdl(paged_join_kernel<__nv_bfloat16, true>, jg, kPagedJoinThreads, 0, st, p)
-                      : launch_pdl(paged_join_kernel<__nv_bfloat16, false>, jg, kPagedJoinThreads, 0, st, p);
+    if (dtype == LA_F32) return weights_in ? paged_join<float, true>(p, pl, st) : paged_join<float, false>(p, pl, st);
+    return weights_in ? paged_join<__nv_bfloat16, true>(p, pl, st) : paged_join<__nv_bfloat16, false>(p, pl, st);
 }
 
 // Most slots that can move in one (b, h): as many as lie below the budget, or above it.

@@ -763,6 +763,15 @@ __device__ __forceinline__ int paged_slot(int r)
 // P enters as two bf16 halves, p = hi + lo (error 2^-17 of p instead of 2^-9).
 // With at most 8 heads (HI false) the low half takes the rows 8..15, which are
 // free, and costs no further MMA.
+// Shared memory to ask for so that not more than `blocks` blocks fit an SM.  The
+// ranges are dealt out for so many: a launch that begins while the last one's
+// join is still leaving some SMs could otherwise put more blocks on the others.
+constexpr int paged_smem(int need, int blocks)
+{
+    const int least = 228 * 1024 / (blocks + 1) - 1024 + 128;
+    return need > least ? need : least;
+}
+
 template <int DQ, int DV, bool HI>
 struct PagedMma {
     static constexpr int KB = DQ / 64, VB = DV / 64;           // 64-column blocks
@@ -773,8 +782,8 @@ struct PagedMma {
     static constexpr int OFF_ML = OFF_O + kPagedWarps * 8 * kPagedMergeCols * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
     static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
-    static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
     static constexpr int BLOCKS = KB > 1 || VB > 1 ? 2 : 3;    // per SM
+    static constexpr int SMEM = paged_smem(OFF_BAR + kPagedWarps * ST * 8, BLOCKS);
     static constexpr int REGS = BLOCKS == 3 ? 168 : HI ? 248 : 224;   // 224: the join fits beside two blocks
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -1034,8 +1043,8 @@ struct PagedSimt {
     static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
     static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
-    static constexpr int SMEM = OFF_BAR + kPagedWarps * ST * 8;
     static constexpr int BLOCKS = D > 64 && GM > 4 && !TMA && sizeof(T) == 4 ? 1 : D > 64 || GM > 4 ? 2 : 3;   // per SM
+    static constexpr int SMEM = paged_smem(OFF_BAR + kPagedWarps * ST * 8, BLOCKS);
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
