@@ -38,8 +38,8 @@
  *    never allocates or frees device memory and never synchronises, except
  *    la_get_device_status.  Work is enqueued on `stream` (a cudaStream_t,
  *    passed as void*; NULL is the legacy default stream) and runs
- *    asynchronously.  The tensor-core forward kernels and the decode kernels
- *    are launched with programmatic stream serialization: each waits for the
+ *    asynchronously.  The tensor-core forward kernels, the decode kernels and
+ *    the paged-cache kernels are launched with programmatic stream serialization: each waits for the
  *    kernel before it in the stream to complete before it touches memory,
  *    and lets the kernel after it be scheduled while it drains.  A kernel of
  *    the caller that follows one of these calls and is itself launched with
