@@ -1106,6 +1106,7 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
     const int sk = paged_slot(r);
     const uint32_t off_k = sk * 128 + ((cq ^ sk) << 4);   // coordinates 16 j + ..: ^ 64 for odd j, + a block per two
     const uint32_t off_v = (vcol / 32) * Cfg::BLOCK;
+    constexpr int F = GM < 4 ? GM : 4;
     float4 o[GM];
     float m[GM], l[GM];
     int t0 = 0;
@@ -1136,6 +1137,8 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
         if (mask && feed.alive) {
             if (t.newrow >= 0) feed.patch(kp, (const T *)p.k + w.bh(p) * c.dqk, (T *)c.kp, c.dqk, Cfg::NB, t);
             const uint32_t ks = smem_addr(kp);
+            // heads go by in groups of four without a branch between them, so that
+            // their loads and sums overlap (a head past `rows` has zeros for a query)
             float s[2][GM];
 #pragma unroll
             for (int n = 0; n < GM; ++n) s[0][n] = s[1][n] = 0.f;
@@ -1145,40 +1148,57 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                 const float4 k0 = lds_f4(ks + (j >> 1) * Cfg::BLOCK + (off_k ^ (j & 1) * 64));
                 const float4 k1 = lds_f4(ks + (j >> 1) * Cfg::BLOCK + 1024 + (off_k ^ (j & 1) * 64));
 #pragma unroll
-                for (int n = 0; n < GM; ++n) {
-                    if (n >= rows) break;
-                    const float4 x = *reinterpret_cast<const float4 *>(qs + n * D + j * 16 + cq * 4);
-                    s[0][n] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[0][n]))));
-                    s[1][n] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[1][n]))));
+                for (int n0 = 0; n0 < GM; n0 += F) {
+                    if (n0 >= rows) break;
+                    float4 x[F];
+#pragma unroll
+                    for (int n = 0; n < F; ++n) x[n] = *reinterpret_cast<const float4 *>(qs + (n0 + n) * D + j * 16 + cq * 4);
+#pragma unroll
+                    for (int n = 0; n < F; ++n) {
+                        float &s0 = s[0][n0 + n], &s1 = s[1][n0 + n];
+                        s0 = fmaf(x[n].x, k0.x, fmaf(x[n].y, k0.y, fmaf(x[n].z, k0.z, fmaf(x[n].w, k0.w, s0))));
+                        s1 = fmaf(x[n].x, k1.x, fmaf(x[n].y, k1.y, fmaf(x[n].z, k1.z, fmaf(x[n].w, k1.w, s1))));
+                    }
                 }
             }
 #pragma unroll
-            for (int n = 0; n < GM; ++n) {
-                if (n >= rows) break;
-                float mx = m[n];
+            for (int n0 = 0; n0 < GM; n0 += F) {
+                if (n0 >= rows) break;
+                float mx[F];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = s[i][n];
-                    x += __shfl_xor_sync(ALL, x, 1);
-                    x += __shfl_xor_sync(ALL, x, 2);
-                    s[i][n] = x = mask >> (i * 8 + sk) & 1 ? x : -INFINITY;
-                    mx = fmaxf(mx, x);
-                    if (p.scores && cq == 0) p.scores[(hq0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + sk] = x;
+                for (int n = 0; n < F; ++n) {
+                    mx[n] = m[n0 + n];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x = s[i][n0 + n];
+                        x += __shfl_xor_sync(ALL, x, 1);
+                        x += __shfl_xor_sync(ALL, x, 2);
+                        s[i][n0 + n] = x = mask >> (i * 8 + sk) & 1 ? x : -INFINITY;
+                        mx[n] = fmaxf(mx[n], x);
+                        if (p.scores && cq == 0 && n0 + n < rows)
+                            p.scores[(hq0 + n0 + n) * p.stride + (w.tile << 6) + warp * 16 + i * 8 + sk] = x;
+                    }
                 }
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, off));
-                const float base = mx == -INFINITY ? 0.f : mx, al = ex2(m[n] - base);
-                m[n] = mx;
-                const float e0 = ex2(s[0][n] - base), e1 = ex2(s[1][n] - base);
-                l[n] = l[n] * al + e0 + e1;
-                if (cq == (n & 3)) {
-                    ps[sk * GM + n] = e0;
-                    ps[(8 + sk) * GM + n] = e1;
+                for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+                    for (int n = 0; n < F; ++n) mx[n] = fmaxf(mx[n], __shfl_xor_sync(ALL, mx[n], off));
+#pragma unroll
+                for (int n = 0; n < F; ++n) {
+                    const int nn = n0 + n;
+                    const float base = mx[n] == -INFINITY ? 0.f : mx[n], al = ex2(m[nn] - base);
+                    m[nn] = mx[n];
+                    const float e0 = ex2(s[0][nn] - base), e1 = ex2(s[1][nn] - base);
+                    l[nn] = l[nn] * al + e0 + e1;
+                    if (cq == (nn & 3)) {
+                        ps[sk * GM + nn] = e0;
+                        ps[(8 + sk) * GM + nn] = e1;
+                    }
+                    o[nn].x *= al;
+                    o[nn].y *= al;
+                    o[nn].z *= al;
+                    o[nn].w *= al;
                 }
-                o[n].x *= al;
-                o[n].y *= al;
-                o[n].z *= al;
-                o[n].w *= al;
             }
             __syncwarp();
             uint8_t *vp = feed.take(t.copies, c.dv);
@@ -1192,7 +1212,6 @@ paged_decode_simt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                     const int row = i * Cfg::TP + vrow;
                     const float4 x = lds_f4(vs + row * 128 + (((lane ^ row) & 7) << 4));
                     const float *pp = ps + row * GM;
-                    constexpr int F = GM < 4 ? GM : 4;   // weights per load
 #pragma unroll
                     for (int n0 = 0; n0 < GM; n0 += F) {
                         if (n0 >= rows) break;
