@@ -742,7 +742,7 @@ static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_si
     pl->gs = (g + pl->nsub - 1) / pl->nsub;
     // as many blocks as an SM holds (BLOCKS of the kernels' configurations)
     const bool narrow = dqk <= 64 && dv <= 64;
-    pl->grid = kNumSms * (narrow && (pl->mma || pl->gs <= 4)                             ? 3
+    pl->grid = kNumSms * (narrow && (pl->mma || pl->gs <= 8)                             ? 3
                           : !narrow && !pl->tma && dtype == LA_F32 && pl->gs > 4 ? 1
                                                                                  : 2);
     pl->tile = pl->mma ? 7 : 6;
@@ -828,10 +828,12 @@ static la_status paged_simt(const PagedDecodeParams &p, const PagedPlan &pl, cud
 {
     if (p.c.dqk <= 64 && p.c.dv <= 64) {
         if (pl.gs == 1) return paged_simt_run<T, 64, 1, TMA>(p, pl, st);
-        return pl.gs <= 4 ? paged_simt_run<T, 64, 4, TMA>(p, pl, st) : paged_simt_run<T, 64, 16, TMA>(p, pl, st);
+        if (pl.gs <= 4) return paged_simt_run<T, 64, 4, TMA>(p, pl, st);
+        return pl.gs <= 8 ? paged_simt_run<T, 64, 8, TMA>(p, pl, st) : paged_simt_run<T, 64, 16, TMA>(p, pl, st);
     }
     if (pl.gs == 1) return paged_simt_run<T, 128, 1, TMA>(p, pl, st);
-    return pl.gs <= 4 ? paged_simt_run<T, 128, 4, TMA>(p, pl, st) : paged_simt_run<T, 128, 16, TMA>(p, pl, st);
+    if (pl.gs <= 4) return paged_simt_run<T, 128, 4, TMA>(p, pl, st);
+    return pl.gs <= 8 ? paged_simt_run<T, 128, 8, TMA>(p, pl, st) : paged_simt_run<T, 128, 16, TMA>(p, pl, st);
 }
 
 template <typename T, bool WEIGHTS>

@@ -1040,11 +1040,11 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 // and 8 + slot(r)), and a lane owns four columns of the output.  Bound by HBM with
 // a head of keys for each query head (16 sequences of up to 4096 slots, 16 heads,
 // d = 64, 303 MB: 57 us a step, 5.3 TB/s), by the issue of FMA from four shared
-// heads on (8 heads, d = 128: 7.5 TFLOP/s).
+// heads on (8 heads, d = 128: 11.7 TFLOP/s).
 template <typename T, int D, int GM, bool TMA>
 struct PagedSimt {
     static constexpr int NB = D / 32;                // 32-column blocks
-    static constexpr int ST = !TMA || (D > 64 && GM > 4) ? 2 : 3;
+    static constexpr int ST = !TMA || (D > 64 && GM > 8) ? 2 : 3;
     static constexpr int OR = GM < 8 ? GM : 8;       // rows merged at once
     using Feed = PagedFeed<T, float, NB, NB, 16, ST, TMA>;
     static constexpr int BLOCK = Feed::BLOCK;
@@ -1055,7 +1055,7 @@ struct PagedSimt {
     static constexpr int OFF_ML = OFF_P + kPagedWarps * 16 * GM * 4;
     static constexpr int OFF_TILE = OFF_ML + kPagedWarps * kPagedRows * 8;
     static constexpr int OFF_BAR = OFF_TILE + kPagedWarps * kPagedAhead * kPagedTileBytes;
-    static constexpr int BLOCKS = D > 64 && GM > 4 && !TMA && sizeof(T) == 4 ? 1 : D > 64 || GM > 4 ? 2 : 3;   // per SM
+    static constexpr int BLOCKS = D > 64 && GM > 4 && !TMA && sizeof(T) == 4 ? 1 : D > 64 || GM > 8 ? 2 : 3;   // per SM
     static constexpr int SMEM = paged_smem(OFF_BAR + kPagedWarps * ST * 8, BLOCKS);
     static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };

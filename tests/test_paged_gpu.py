@@ -85,6 +85,8 @@ SHAPES = [  # dtype, Hq, Hkv, dqk, dv, page
     (F32, 4, 4, 64, 64, 16), (F32, 8, 2, 128, 128, 64), (F32, 20, 1, 64, 32, 8), (F32, 6, 3, 24, 40, 10),
     (F32, 5, 1, 33, 20, 7), (F32, 1, 1, 1, 128, 1), (F32, 17, 1, 128, 128, 128),
     (BF16, 128, 1, 64, 64, 16), (F32, 65, 1, 32, 40, 4), (BF16, 6, 2, 65, 127, 48), (F32, 9, 3, 127, 66, 2),
+    (F32, 2, 1, 4, 8, 16), (F32, 14, 2, 128, 64, 256), (F32, 5, 1, 64, 64, 12), (BF16, 12, 1, 96, 24, 128),
+    (F32, 8, 1, 65, 33, 32), (BF16, 10, 1, 128, 127, 5), (BF16, 64, 8, 64, 64, 200),
 ]
 
 
