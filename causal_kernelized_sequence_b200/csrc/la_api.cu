@@ -106,7 +106,8 @@ la_status launch_status()
 // the grid may be scheduled onto SMs that kernel has left once all its blocks
 // have started (every tensor-core forward kernel triggers at its start), and
 // each of these kernels waits for the previous one to complete (its writes
-// visible) before it touches global memory.
+// visible) before it touches global memory.  cluster > 1: in clusters of so many
+// blocks.
 template <typename... KArgs, typename... Args>
 la_status launch_pdl_cluster(void (*kernel)(KArgs...), int grid, int threads, int smem, int cluster, cudaStream_t stream,
                              Args &&...args)
