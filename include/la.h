@@ -396,8 +396,7 @@ LA_API size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, i
  *      positions[b,h,lens[b]] = pos[b].
  *   workspace at least la_paged_decode_workspace_bytes(...) bytes.
  * Where nothing is attended to (n = 0, only pages out of range, or every score
- * -inf) y = 0 and lse = -inf.  Slots past n are not read: what stale pages
- * hold does not matter.
+ * -inf) y = 0 and lse = -inf.  What slots past n hold does not matter.
  * Errors: LA_ERR_INVALID_ARG also when Hq is not a multiple of Hkv;
  * LA_ERR_UNSUPPORTED for more than 128 query heads per key/value head. */
 LA_API la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse,
