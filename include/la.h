@@ -397,6 +397,9 @@ LA_API size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, i
  *   workspace at least la_paged_decode_workspace_bytes(...) bytes.
  * Where nothing is attended to (n = 0, only pages out of range, or every score
  * -inf) y = 0 and lse = -inf.  What slots past n hold does not matter.
+ * Infinite values count as they stand in the sum: with a weight above 0 their
+ * infinity (NaN beside the other one), with weight 0 NaN; a weight below 2^-110
+ * of the row's largest may count as 0.
  * Errors: LA_ERR_INVALID_ARG also when Hq is not a multiple of Hkv;
  * LA_ERR_UNSUPPORTED for more than 128 query heads per key/value head. */
 LA_API la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse,
