@@ -1327,7 +1327,7 @@ la_status la_paged_cache_fill(const void *k, const void *v, void *k_pages, void 
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(n_new, 4) || !aligned(weights, 4) ||
         !aligned(positions, 4) || !aligned(pos, 4) || (positions == nullptr) != (pos == nullptr))
         return LA_ERR_INVALID_ARG;
-    const int64_t blocks = (int64_t)B * Hkv * (((int64_t)N + kPagedFillRows - 1) / kPagedFillRows);
+    const int64_t blocks = (int64_t)B * Hkv * paged_fill_tiles(N);
     if (blocks >= (int64_t)1 << 31) return LA_ERR_INVALID_ARG;
     if (check_on_current_device(k_pages) != LA_OK) return LA_ERR_INVALID_ARG;
     PagedFillParams p;

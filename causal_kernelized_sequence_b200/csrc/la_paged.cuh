@@ -35,6 +35,10 @@ __device__ __forceinline__ int paged_row(const PagedCache &c, int b, int h, int 
 
 constexpr int kPagedFillThreads = 256;
 constexpr int kPagedFillRows = 64;
+// Blocks that a head's N tokens take, for every N (N + 63 may pass 31 bits).
+__host__ __device__ constexpr int paged_fill_tiles(int N) { return (N - 1) / kPagedFillRows + 1; }
+static_assert(paged_fill_tiles(1) == 1 && paged_fill_tiles(64) == 1 && paged_fill_tiles(65) == 2, "paged_fill_tiles");
+static_assert(paged_fill_tiles(INT_MAX) == 1 << 25, "paged_fill_tiles");
 
 struct PagedFillParams {
     PagedCache c;
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
     sm100::launch_dependents();
     __shared__ int rows[kPagedFillRows];
     const PagedCache &c = p.c;
-    const int tiles = (p.N + kPagedFillRows - 1) / kPagedFillRows;
+    const int tiles = paged_fill_tiles(p.N);
     const int bh = blockIdx.x / tiles, i0 = (blockIdx.x - bh * tiles) * kPagedFillRows;
     const int b = bh / c.Hkv, h = bh - b * c.Hkv;
     const int tid = threadIdx.x;

@@ -78,3 +78,22 @@ def test_infinite_value_of_the_new_token(Hq):
     sync()
     assert (y[..., 0] == math.inf).all() and (y[..., 1] == -math.inf).all()
     check_step(BF16, 5001, d, (y[..., 2:], lse, None), (ref[0][..., 2:], ref[1], None, ref[3][..., 2:], ref[4]))
+
+
+# ---------------------------------------------------- what a call leaves alone
+
+def test_append_from_the_longest_padded_batch():
+    """N = 2^31 - 1 tokens of padding, of which n_new count: both heads' first tokens are stored and nothing else."""
+    N, Hkv, page, held, new = (1 << 31) - 1, 2, 16, 5, 70
+    k = torch.empty(1, Hkv, N, 1, dtype=BF16, device=DEV)
+    v = torch.empty(1, Hkv, N, 1, dtype=BF16, device=DEV)
+    for i, t in enumerate((k, v)):
+        t[:, :, :new] = torch.randn(1, Hkv, new, 1, generator=torch.Generator().manual_seed(i)).to(BF16).to(DEV)
+    kp, vp = (torch.randn(8, Hkv, page, 1, generator=torch.Generator().manual_seed(9 + i)).to(BF16) for i in range(2))
+    table = torch.tensor([[3, 0, 6, 1, 5, -1]], dtype=torch.int32)
+    lens, n_new = torch.tensor([held], dtype=torch.int32), torch.tensor([new], dtype=torch.int32)
+    kr, vr, _, _ = orc.fill(k[:, :, :new].cpu(), v[:, :, :new].cpu(), kp, vp, table, lens, n_new)
+    kpd, vpd, td, ld, nd = to_dev(kp, vp, table, lens, n_new)
+    la.la_paged_cache_fill(k, v, kpd, vpd, td, ld, n_new=nd)
+    sync()
+    assert torch.equal(kpd.cpu(), kr) and torch.equal(vpd.cpu(), vr)
