@@ -18,6 +18,7 @@
 #include <utility>
 
 #include "la_device.cuh"
+#include "la_raise.cuh"
 #include "la_simt.cuh"
 #include "la_decode.cuh"
 #include "la_prefill_sm100.cuh"
@@ -142,24 +143,22 @@ la_status launch_pdl(void (*kernel)(KArgs...), int grid, int threads, int smem, 
 
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device) and
 // size; later calls (for example during CUDA-graph capture) make no API call.
-// The table is atomic because calls may come from several host threads; two
-// threads racing on a first call both set the same attribute, which is harmless.
+// Calls may come from several host threads, and with different sizes.
 template <auto kernel>
 la_status set_smem(size_t bytes)
 {
     if (bytes <= 48 * 1024) return LA_OK;
-    static std::atomic<size_t> done[64];  // one table per kernel, zero-initialised
+    static Raise limit[64];  // one table per kernel
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LA_ERR_CUDA;
-    if (done[dev].load(std::memory_order_acquire) >= bytes) return LA_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-        return LA_ERR_CUDA;
-    done[dev].store(bytes, std::memory_order_release);
-    return LA_OK;
+    const bool ok = limit[dev].to(bytes, [](size_t n) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n) == cudaSuccess;
+    });
+    return ok ? LA_OK : LA_ERR_CUDA;
 }
 
 // Ask for the SM's whole shared memory beside a kernel that uses little of it
-// (once per kernel and device, as above).  A launch that begins while the
+// (once per kernel and device; two threads set the same).  A launch that begins while the
 // kernel's last blocks leave would otherwise find SMs divided for the little,
 // and could place fewer of its blocks there until they are empty.
 template <auto kernel>
