@@ -1472,15 +1472,8 @@ la_status la_paged_evict(void *k_pages, void *v_pages, const int32_t *block_tabl
     p.newlen = lens_out == lens ? p.movers + (size_t)B * Hkv * p.maxmoves : nullptr;
     p.elem = (int)elem_size(dtype);
     p.width = rows16(dqk, dtype) && rows16(dv, dtype) ? 16 : p.elem;
-    // blocks per (b, h): as many as run at once (four on an SM), with at least 1024
-    // slots each, and so many that the keys of twice the budget fit their shared
-    // memory (a longer sequence is right too: its keys are made anew in each sweep)
     const int64_t units = (int64_t)B * Hkv, cap = (int64_t)max_pages * page_size;
-    const int64_t likely = cap < 2 * (int64_t)budget + 1024 ? cap : 2 * (int64_t)budget + 1024;
-    int cs = 1;
-    while (cs < kEvictMaxCluster &&
-           ((units * cs * 2 <= 4 * kNumSms && cap >= (int64_t)cs * 2 * 1024) || likely > (int64_t)cs * kEvictMaxKeys))
-        cs *= 2;
+    const int cs = paged_evict_cluster(units, cap, budget);
     if (units * cs >= (int64_t)1 << 31) return LA_ERR_INVALID_ARG;
     const int64_t slice = (cap + cs * kEvictThreads - 1) / (cs * kEvictThreads) * kEvictThreads;
     p.keys = (int)(slice < kEvictMaxKeys ? slice : kEvictMaxKeys);

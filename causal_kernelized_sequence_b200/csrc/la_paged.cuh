@@ -1542,6 +1542,44 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxKeys = 12288;
 constexpr int kEvictMaxCluster = 8;
 
+// Blocks per (b, h) of an eviction, `units` of them, of tables of `cap` slots: more
+// while
+//   - all blocks run at once, with at least 1024 slots each.  Clusters have two
+//     blocks on an SM and lie within a GPC: 144 of 2, 64 of 4 and 32 of 8 ran at
+//     once, 152, 74 and 40 did not.  2112 -> 2048 slots, 152 heads: 12 us alone, 23
+//     in clusters of 2; 8256 -> 8192, 74 heads: 23 alone, 19 of 2, 27 of 4; 64 heads
+//     of 32,768 -> 4096: 76 of 4, 86 of 8.  (Where a fourth of the slots stays, the
+//     rows weigh more and a second round is about even: 8192 -> 2048, 200 heads: 108
+//     alone, 96 of 2; 512 heads 215 and 205.)  Blocks of fewer slots cost more than they
+//     save (1088 -> 1024: 9.4 alone, 11.7 of 2; at 2112 -> 2048 it is 11 to 13, but
+//     where half the slots go, 22 to 18).
+//   - or the table's keys do not fit the blocks' shared memory and the blocks run in
+//     two rounds: keys are then made anew in each sweep (32,768 -> 4096, 144 heads:
+//     310 of 2, 177 of 4).
+//   - or the keys of twice the budget do not fit, however many blocks that takes.
+//     A longer sequence is right too; that cap itself fits is not asked for, since a
+//     table may be far wider than what it holds (512 heads of 32,768 -> 4096: 1396
+//     alone, 506 of 4; but 4160 -> 4096 in the same table 22 and 102).
+constexpr int paged_evict_cluster(long long units, long long cap, long long budget)
+{
+    const long long likely = cap < 2 * budget + 1024 ? cap : 2 * budget + 1024;
+    int cs = 1;
+    while (cs < kEvictMaxCluster) {
+        const long long more = cs * 2, keys = (long long)cs * kEvictMaxKeys;
+        const bool at_once = units * more <= (more == 2 ? 288 : 256) && cap >= more * 1024;
+        const bool two_rounds = cap > keys && units * more <= 592;
+        if (!at_once && !two_rounds && likely <= keys) break;
+        cs = (int)more;
+    }
+    return cs;
+}
+static_assert(paged_evict_cluster(512, 2112, 2048) == 1 && paged_evict_cluster(152, 2112, 2048) == 1 &&
+                  paged_evict_cluster(144, 2112, 2048) == 2 && paged_evict_cluster(32, 32768, 4096) == 8 &&
+                  paged_evict_cluster(64, 32768, 4096) == 4 && paged_evict_cluster(74, 8256, 8192) == 2 &&
+                  paged_evict_cluster(144, 32768, 4096) == 4 && paged_evict_cluster(512, 32768, 4096) == 1 &&
+                  paged_evict_cluster(4096, 1 << 20, 1 << 19) == 8,
+              "paged_evict_cluster");
+
 // Weight as an unsigned key of the same order: larger weight, larger key; NaN
 // counts as -inf and -0 as +0.  No weight has the key 0 or 2^32 - 1.
 __device__ __forceinline__ uint32_t weight_key(float w)

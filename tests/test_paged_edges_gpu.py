@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import causal_kernelized_sequence_b200 as la
+import test_paged_gpu as base
 from oracle import paged as orc
 from test_paged_gpu import BF16, DEV, F32, U, cache, check_step, sync, to_dev
 
@@ -97,3 +98,15 @@ def test_append_from_the_longest_padded_batch():
     la.la_paged_cache_fill(k, v, kpd, vpd, td, ld, n_new=nd)
     sync()
     assert torch.equal(kpd.cpu(), kr) and torch.equal(vpd.cpu(), vr)
+
+
+# ------------------------------------------------------------------- evictions
+
+@pytest.mark.parametrize("B,Hkv,n,budget,recent,ties", [
+    (20, 8, 20000, 3000, 100, True),        # more clusters of 2 than run at once
+    (9, 8, 26000, 2000, 0, False),          # more clusters of 4
+    (152, 1, 9000, 8000, 500, True),        # single blocks with long slices
+    (8, 5, 9000, 4500, 64, False)])         # clusters of 4 for tables that could take 8
+def test_evict_by_blocks_and_clusters(B, Hkv, n, budget, recent, ties):
+    """The same answer whatever number of blocks shares a head."""
+    base.test_evict_long(B, Hkv, n, budget, recent, ties)
