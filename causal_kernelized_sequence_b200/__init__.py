@@ -470,13 +470,17 @@ def la_swa_decode_step(q, k, v, k_cache, v_cache, pos, window, y=None):
 
 
 _paged_sizes = {}   # workspace sizes by their arguments: asked for at every step
+_PAGED_SIZES = 1024   # kept at most; a server meets new batch sizes and table widths for as long as it runs
 
 
 def _paged_workspace(fn, workspace, device, *sizes):
     """(pointer, bytes, keep-alive) of the workspace a paged call needs."""
     need = _paged_sizes.get((fn, sizes))
     if need is None:
-        need = _paged_sizes[(fn, sizes)] = int(getattr(load_library(), fn)(*sizes))
+        need = int(getattr(load_library(), fn)(*sizes))
+        if len(_paged_sizes) >= _PAGED_SIZES:
+            _paged_sizes.clear()
+        _paged_sizes[(fn, sizes)] = need
     if workspace is None and not need:
         return None, 0, None
     workspace, have = _workspace(workspace, need, device)
