@@ -752,10 +752,22 @@ static la_status paged_plan(int B, int Hq, int Hkv, int dqk, int dv, int page_si
     if (units >= (int64_t)1 << 31 || (double)tiles * units / pl->grid >= 2e9) return LA_ERR_INVALID_ARG;
     // Short sequences: one unit per block needs neither a scan over the lengths nor
     // a join, and the hardware deals the blocks out; with many units the blocks'
-    // starts cost more.  Measured, one block per unit against ranges and join, at
-    // up to 512 slots: d = 64, 1024 units 26.7 us against 30.7, 4096 units 82.3
-    // against 84.0; d = 128, 960 units 41.9 against 46.4, 4096 units 141 against 136.
-    pl->aligned = !weights && tiles <= 4 && units <= 6 * pl->grid;
+    // starts cost more, and with few long ones the others idle.  How long they are
+    // only the device knows, so the table's width decides.  Measured, us a step, one
+    // block per unit / ranges and join, ragged lengths up to the tiles given:
+    //   bf16 d = 64, 4 heads a unit         3 tiles    4 tiles    5 tiles    8 tiles
+    //       4 units                         7.9/7.9    9.7/8.2    11.5/8.3   16.9/8.9
+    //       64                              8.1/9.9    10.2/10.4  11.8/10.4  17.4/11.2
+    //       256                             9.2/12.7   11.5/15.0  13.5/15.8  19.8/18.6
+    //       1024                            20.4/24.2  24.0/27.3  28.6/31.1  39.0/41.5
+    //   bf16 d = 128, 4 heads, 128 units    10.7/13.5  12.9/14.2  14.9/14.1  21.5/18.1
+    //       1024                            35.4/38.8  42.1/44.2  46.1/49.9  66.5/63.6
+    //       2048                            62.0/64.9  73.2/74.0  84.2/85.9  110/109
+    //   fp32 d = 64, one head, 256 units    8.6/12.0   10.7/15.5  12.5/15.2  18.3/18.2
+    //       4096                            58.5/60.7  69.2/68.9  82.0/81.0  108/106
+    // (bf16 d = 128, 16 heads, 256 units: 16.2/41.0, 18.9/45.3, 21.4/48.7, 29.1/56.1:
+    // a unit's end weighs more there than its cost says.)
+    pl->aligned = !weights && tiles <= 4 && units <= 6 * pl->grid;   // (the weights need the join)
     if (pl->aligned) pl->grid = (int)units;
     return LA_OK;
 }

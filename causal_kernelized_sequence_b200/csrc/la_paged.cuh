@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kPagedFillThreads) paged_fill_kernel(const Pag
 // go to the workspace and the join kernel adds them, in the order of the ranges:
 // with M = max m_i,
 //     y = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i      (scores in log2 units).
+// O and l are formed before the division, so values above the type's largest over
+// the number of slots can overflow.
 // The same launch then adds the normalised weights, from the step's scores
 // kept in the workspace: a weight needs the whole row's sum.
 
@@ -334,7 +336,8 @@ __device__ __forceinline__ bool paged_range(const PagedDecodeParams &p, PagedWal
     return true;
 }
 
-// 2^x; results below 2^-126 are 0.
+// 2^x to 2^-22 of itself (two units of fp32; the function of the libraries has one,
+// at some ten instructions for each score); results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -813,12 +816,23 @@ __device__ __forceinline__ int paged_slot(int r)
 // sum, so p is cut off and the low half kept above 0 (error 2^-16).  Finding
 // infinite values by a vote instead, which keeps 2^-17, took 35 us instead of 31
 // (16 sequences of 8192, 16 heads, d = 128) and 76 instead of 63 (4096, 72 on 8).
+// A score's products are exact and its sum is the tensor core's, which adds 16 of
+// them at a time in fp32 and may cut off where FMA would round.  Neither these nor
+// P's halves show beside y's own rounding (2^-9): against 64 bits y is 0.0017 of
+// its norm off, as is a form that holds all of them in fp32.
 //
 // Bound by HBM at long contexts: 131,072 slots, 32 query heads on 8, d = 128
-// (537 MB) take 91 us a step, join included, 5.9 TB/s.  A chunk of 32 slots is
+// (537 MB) take 90 us a step, join included, 5.9 TB/s.  A chunk of 32 slots is
 // about 750 warp instructions; with chunks of 16 (590 each) eight warps per SM
 // issued too slowly, 127 us.  Short contexts are bound by a block's chain of
 // latencies: about 3 us to its first rows, 1.7 us a tile, 1.3 us a unit's end.
+// With 9 to 16 heads two warps on a scheduler do not hide their own latencies: 16
+// sequences of 4096, 128 heads on 8, d = 128 (268 MB) take 74 us a step, 56 % of
+// the measured copy bandwidth, with the tensor pipe at 23 % and a scheduler issuing
+// in one cycle of three; an instruction waits 2.1 cycles for fixed latencies, 0.6 for
+// shared memory.  Groups above 16 read their keys again for each 16 heads, from L2: 8
+// sequences of 16,384, 128 heads on one, 104 us, DRAM 78 MB for 67 of keys and values.
+
 // Shared memory to ask for so that not more than `blocks` blocks fit an SM.  The
 // ranges are dealt out for so many: a launch that begins while the last one's
 // join is still leaving some SMs could otherwise put more blocks on the others.
@@ -1084,10 +1098,17 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 // fp32, and bf16 rows that do not start on 16-byte boundaries: the same walk
 // with fp32 FMA on four floats per 16-byte piece.  A quad of lanes shares a slot
 // in the scores (lane c holds the coordinates 16 j + 4 c .. + 3 of slots slot(r)
-// and 8 + slot(r)), and a lane owns four columns of the output.  Bound by HBM with
-// a head of keys for each query head (16 sequences of up to 4096 slots, 16 heads,
-// d = 64, 303 MB: 57 us a step, 5.3 TB/s), by the issue of FMA from four shared
-// heads on (8 heads, d = 128: 11.7 TFLOP/s).
+// and 8 + slot(r)), and a lane owns four columns of the output.  The queries are
+// scaled to log2 units in fp32 before the products, one rounding of each, where the
+// scores would take one each.
+// Bound by HBM with a head of keys for each query head (16 sequences of up to 4096
+// slots, 16 heads, d = 64, 303 MB: 57 us a step, 5.3 TB/s), with shared heads by the
+// latencies that two warps on a scheduler leave open: 16 sequences of 2048, 64 heads
+// on 8, d = 128 (268 MB) take 97 us a step, the FMA pipe at 22 % and a scheduler
+// issuing in two cycles of five; an instruction waits 1.2 cycles for fixed latencies
+// and 1.1 for shared memory (a query read of 16 bytes feeds 8 FMA).  Rows off 16 bytes are bound
+// the same way by their spreading: bf16 d = 127, 16 sequences of 4096, 8 heads (266
+// MB) 243 us, fixed latencies 1.9 cycles, shared memory 1.4.
 template <typename T, int D, int GM, bool TMA>
 struct PagedSimt {
     static constexpr int NB = D / 32;                // 32-column blocks
@@ -1545,8 +1566,8 @@ constexpr int kEvictMaxCluster = 8;
 // Blocks per (b, h) of an eviction, `units` of them, of tables of `cap` slots: more
 // while
 //   - all blocks run at once, with at least 1024 slots each.  Clusters have two
-//     blocks on an SM and lie within a GPC: 144 of 2, 64 of 4 and 32 of 8 ran at
-//     once, 152, 74 and 40 did not.  2112 -> 2048 slots, 152 heads: 12 us alone, 23
+//     blocks on an SM and lie within a GPC: 144 of 2, 64 of 4 and 31 of 8 ran at
+//     once, 152 and 74 did not, and 32 of 8 are still no slower than of 4.  2112 -> 2048 slots, 152 heads: 12 us alone, 23
 //     in clusters of 2; 8256 -> 8192, 74 heads: 23 alone, 19 of 2, 27 of 4; 64 heads
 //     of 32,768 -> 4096: 76 of 4, 86 of 8.  (Where a fourth of the slots stays, the
 //     rows weigh more and a second round is about even: 8192 -> 2048, 200 heads: 108
@@ -1658,19 +1679,26 @@ __device__ __forceinline__ int warps_before(int x, int *part, int &total)
     return __shfl_sync(0xffffffffu, s, warp) - x;
 }
 
-// One cluster of blocks per (b, h), each block with a slice of the slots.  The
-// order is one of 32-bit keys: a recent token's is the largest, the others
-// follow their weights.  A radix select (11, 11 and 10 bits; the blocks add
-// their histograms over distributed shared memory) finds the smallest key that
-// is kept and how many slots of that key are; sweeps in slot order then rank
-// the ties, list the dropped slots below the budget and the kept ones above it,
-// and move rows, weights and positions along the two lists.  Sources lie at or
-// above the budget and destinations below it, so moves need no order.
+// One block, or a cluster of them, per (b, h), each block with a slice of the slots.
+// The order is one of 32-bit keys: a recent token's is the largest, the others
+// follow their weights.  A radix select (one block: digits of 11, 11 and 10 bits; a
+// cluster: four of 8, its blocks adding their histograms over distributed shared
+// memory) finds the smallest key that is kept and how many slots of that key are;
+// sweeps in slot order then rank the ties, list the dropped slots below the budget
+// and the kept ones above it, and move rows, weights and positions along the two
+// lists.  Sources lie at or above the budget and destinations below it, so moves
+// need no order.
 //
-// One page over a budget of 2048, 512 heads of d = 128: 18.6 us, all blocks at
-// once, each a chain of latencies (keys 2 us, select 4, lists 3, rows 2).  32,768
-// slots to 4096, 32 heads, clusters of 8: 43.5 us, of which the rows (117 MB) take
-// 12 at the HBM rate and the select and lists, seven cluster barriers, 24.
+// One page over a budget of 2048, 512 heads of d = 128: 16.7 us a call in a row (20
+// through the binding, 21 in place, with lens written by a second launch).  All
+// blocks run at once, each a chain of latencies: its average end is at 13.1 us
+// (start 0.7, keys and table 2.8, select 3.8, counts 1.7, lists 2.0, rows 2.1), the
+// last at 16.2, because the select's passes differ from head to head.  32,768 slots
+// to 4096, 32 heads, clusters of 8: 48 us in a row, 50 through the binding.  31 of
+// the 32 clusters run at once and end at 40 (start 1.6, keys and table 6.1, select
+// 8.0, counts 1.9, lists 5.5, rows 13.3 on average), the last one begins at 31 and
+// overlaps the next call; seven cluster barriers are in these figures, and the rows
+// (117 MB) alone would take 18 at the measured copy rate.
 template <int U, int BLOCKS, bool CLUSTER>
 __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(const PagedEvictParams p)
 {

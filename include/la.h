@@ -372,8 +372,10 @@ LA_API la_status la_paged_cache_fill(const void *k, const void *v, void *k_pages
                                      int max_pages, int dtype, void *stream);
 
 /* Bytes of device workspace la_paged_decode_step needs: the partial results of
- * sequences that are split across thread blocks and, with_weights != 0, the
- * scores of the step.  The rules of la_forward_workspace_bytes. */
+ * sequences that are split across thread blocks (at most 5 MB) and, with_weights
+ * != 0, the scores of the step, 4 * B * Hq * max_pages * page_size bytes.  It
+ * goes by the table's width, not by lens: 64 sequences, 32 heads and tables of
+ * 131,072 slots take 1.1 GB.  The rules of la_forward_workspace_bytes. */
 LA_API size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, int dv, int page_size, int max_pages,
                                               int with_weights, int dtype);
 
@@ -399,7 +401,12 @@ LA_API size_t la_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int dqk, i
  * -inf) y = 0 and lse = -inf.  What slots past n hold does not matter.
  * Infinite values count as they stand in the sum: with a weight above 0 their
  * infinity (NaN beside the other one), with weight 0 NaN; a weight below 2^-110
- * of the row's largest may count as 0.
+ * of the row's largest may count as 0.  The sums are formed before they are
+ * divided by the sum of exponentials (which is at most n), so values above
+ * FLT_MAX / n may overflow.
+ * The plan of a call (la_paged_kernel_plan) follows its sizes, the table's width
+ * among them, not lens: tables of at most 512 slots (fp32, or rows off 16 bytes:
+ * 256) take one launch where the units are not too many.
  * Errors: LA_ERR_INVALID_ARG also when Hq is not a multiple of Hkv;
  * LA_ERR_UNSUPPORTED for more than 128 query heads per key/value head. */
 LA_API la_status la_paged_decode_step(const void *q, const void *k, const void *v, void *y, float *lse,
