@@ -336,8 +336,8 @@ __device__ __forceinline__ bool paged_range(const PagedDecodeParams &p, PagedWal
     return true;
 }
 
-// 2^x to 2^-22 of itself (two units of fp32; the function of the libraries has one,
-// at some ten instructions for each score); results below 2^-126 are 0.
+// 2^x to within 2^-22 of itself, four half steps of fp32, in one instruction: a
+// score's own error is larger.  Results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -1106,9 +1106,9 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_c
 // latencies that two warps on a scheduler leave open: 16 sequences of 2048, 64 heads
 // on 8, d = 128 (268 MB) take 97 us a step, the FMA pipe at 22 % and a scheduler
 // issuing in two cycles of five; an instruction waits 1.2 cycles for fixed latencies
-// and 1.1 for shared memory (a query read of 16 bytes feeds 8 FMA).  Rows off 16 bytes are bound
-// the same way by their spreading: bf16 d = 127, 16 sequences of 4096, 8 heads (266
-// MB) 243 us, fixed latencies 1.9 cycles, shared memory 1.4.
+// and 1.1 for shared memory (a query read of 16 bytes feeds 8 FMA).  Rows off 16
+// bytes are bound the same way by their spreading: bf16 d = 127, 16 sequences of
+// 4096, 8 heads (266 MB) 243 us, fixed latencies 1.9 cycles, shared memory 1.4.
 template <typename T, int D, int GM, bool TMA>
 struct PagedSimt {
     static constexpr int NB = D / 32;                // 32-column blocks
@@ -1566,14 +1566,14 @@ constexpr int kEvictMaxCluster = 8;
 // Blocks per (b, h) of an eviction, `units` of them, of tables of `cap` slots: more
 // while
 //   - all blocks run at once, with at least 1024 slots each.  Clusters have two
-//     blocks on an SM and lie within a GPC: 144 of 2, 64 of 4 and 31 of 8 ran at
-//     once, 152 and 74 did not, and 32 of 8 are still no slower than of 4.  2112 -> 2048 slots, 152 heads: 12 us alone, 23
-//     in clusters of 2; 8256 -> 8192, 74 heads: 23 alone, 19 of 2, 27 of 4; 64 heads
-//     of 32,768 -> 4096: 76 of 4, 86 of 8.  (Where a fourth of the slots stays, the
-//     rows weigh more and a second round is about even: 8192 -> 2048, 200 heads: 108
-//     alone, 96 of 2; 512 heads 215 and 205.)  Blocks of fewer slots cost more than they
-//     save (1088 -> 1024: 9.4 alone, 11.7 of 2; at 2112 -> 2048 it is 11 to 13, but
-//     where half the slots go, 22 to 18).
+//     blocks on an SM and lie within a GPC: 144 of 2 and 64 of 4 ran at once, 32 of
+//     8 mostly did; 152, 74 and 40 did not.  2112 -> 2048 slots, 152 heads: 12 us
+//     alone, 23 in clusters of 2; 8256 -> 8192, 74 heads: 23 alone, 19 of 2, 27 of 4;
+//     64 heads of 32,768 -> 4096: 76 of 4, 86 of 8.  (Where a fourth of the slots
+//     stays, the rows weigh more and a second round is about even: 8192 -> 2048, 200
+//     heads: 108 alone, 96 of 2; 512 heads 215 and 205.)  Blocks of fewer slots cost
+//     more than they save (1088 -> 1024: 9.4 alone, 11.7 of 2; at 2112 -> 2048 it is
+//     11 to 13, but where half the slots go, 22 to 18).
 //   - or the table's keys do not fit the blocks' shared memory and the blocks run in
 //     two rounds: keys are then made anew in each sweep (32,768 -> 4096, 144 heads:
 //     310 of 2, 177 of 4).
@@ -1693,12 +1693,12 @@ __device__ __forceinline__ int warps_before(int x, int *part, int &total)
 // through the binding, 21 in place, with lens written by a second launch).  All
 // blocks run at once, each a chain of latencies: its average end is at 13.1 us
 // (start 0.7, keys and table 2.8, select 3.8, counts 1.7, lists 2.0, rows 2.1), the
-// last at 16.2, because the select's passes differ from head to head.  32,768 slots
-// to 4096, 32 heads, clusters of 8: 48 us in a row, 50 through the binding.  31 of
-// the 32 clusters run at once and end at 40 (start 1.6, keys and table 6.1, select
-// 8.0, counts 1.9, lists 5.5, rows 13.3 on average), the last one begins at 31 and
-// overlaps the next call; seven cluster barriers are in these figures, and the rows
-// (117 MB) alone would take 18 at the measured copy rate.
+// last at 16.2; the select's end alone lies between 4.8 and 9.6.  32,768 slots to
+// 4096, 32 heads, clusters of 8: 48 us in a row, 50 through the binding.  The blocks
+// end at 36 on average and the last at 41 (start 0.6, keys and table 6.0, select 8.0,
+// counts 2.0, lists 5.6, rows 13.3), but in about one call of three a cluster finds
+// no place and begins at 31.  Seven cluster barriers are in these figures, and the
+// rows (117 MB) alone would take 18 at the measured copy rate.
 template <int U, int BLOCKS, bool CLUSTER>
 __global__ void __launch_bounds__(kEvictThreads, BLOCKS) paged_evict_kernel(const PagedEvictParams p)
 {
